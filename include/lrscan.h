@@ -386,6 +386,76 @@ int lrscan_plan_gated(int64_t B, int64_t T, int64_t D, int dtype, int dir, int a
                       const lrscan_opts *opts, lrscan_plan_info *info);
 
 /*
+ * A [B, T, D] tensor whose D elements of a token are contiguous; element
+ * (b, t, d) is at ptr + b*stride_b + t*stride_t + d (strides in elements, not
+ * negative).  So a call reads or writes a slice of a wider projection in
+ * place.  An input may repeat rows (stride 0); an output's rows must not
+ * overlap.  Rows and base pointers on 16-byte boundaries and an even D take
+ * bulk copies; anything else aligned to its elements takes plain loads.
+ */
+typedef struct lrscan_rows {
+    void *ptr;
+    int64_t stride_b, stride_t;
+} lrscan_rows;
+
+/*
+ * Gated linear recurrence: the scan whose decays and inputs come from gates
+ * (the gate of triton_training_scan.py's model family, a = exp(-8 softplus(x)
+ * r)), computed in the same pass.  r, i, x: [B, T, D] in the storage dtype, the
+ * two gates before their sigmoid and the input; lam: fp32 [D]; c: the decay's
+ * scale (8 in those models), positive.
+ *
+ *   forward   rg = sigmoid(r), ig = sigmoid(i), a = exp(-c softplus(lam) rg)
+ *             h_t = a_t h_{t-1} + sqrt(1 - a_t^2) ig_t x_t,  h_{-1} = h0
+ *             out[b,t,d] = h_t (storage dtype), last = h_{T-1} (fp32, optional)
+ *             where segment_pos is 0, a_t = 0 (so h_t = ig_t x_t, whatever the
+ *             state before: an infinity or NaN there does not pass)
+ *             a token that must leave the state as it is: r = -inf (a = 1 and
+ *             b = 0 exactly; the regrouped state agrees to rounding)
+ *   backward  g_t = grad_out_t + a_{t+1} g_{t+1}, grad_last entering at T-1;
+ *             q = a g (h_{t-1} - ig x a / sqrt(1 - a^2)) log a (0 where
+ *             segment_pos is 0), grad_r = q (1 - rg), grad_x = g sqrt(1 - a^2)
+ *             ig, grad_i = grad_x x (1 - ig), grad_lam = sigmoid(lam) /
+ *             softplus(lam) sum_{b,t} q (fp32 [D]), grad_h0 = a_0 g_0
+ *
+ * State, maps and sums are fp32.  saved (fp32 [B, ceil(T/64), D], optional):
+ * the state before tokens 0, 64, 128, ..., from which the backward makes the
+ * states again, so it reads no output and no rounding of one; the backward
+ * needs it, and takes h0 from its first row (state->h0 is not read).  The
+ * logistic functions, the decay and the square root are accurate to a few
+ * units of fp32 (1 - a to its own rounding).  Two calls agree bit for bit.
+ * Moves 4 elements per (t, d) forward and 7 backward.  With T == 0 the
+ * forward copies h0 (or zeros) into last, the backward grad_last (or zeros)
+ * into grad_h0 and zeros into grad_lam.
+ *
+ * Scratch of lrscan_gates_workspace_bytes(..., dir) bytes (0 for a forward of
+ * one tile): library-owned per (device, stream), or opts->workspace (the other
+ * options are not read).  Waits, streams, capture and errors as
+ * lrscan_fwd_ex.
+ */
+int lrscan_fwd_gates(const lrscan_rows *r, const lrscan_rows *i, const lrscan_rows *x,
+                     const float *lam, float c, const lrscan_rows *out, float *last, float *saved,
+                     const lrscan_state *state, int64_t B, int64_t T, int64_t D, int dtype,
+                     void *stream, const lrscan_opts *opts);
+int lrscan_bwd_gates(const lrscan_rows *r, const lrscan_rows *i, const lrscan_rows *x,
+                     const float *lam, float c, const float *saved, const lrscan_rows *grad_out,
+                     const lrscan_rows *grad_r, const lrscan_rows *grad_i, const lrscan_rows *grad_x,
+                     float *grad_lam, const lrscan_state *state, int64_t B, int64_t T, int64_t D, int dtype,
+                     void *stream, const lrscan_opts *opts);
+size_t lrscan_gates_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype, int dir);
+/*
+ * One token of each of B running requests (r, i, x, out: rows b at stride_b,
+ * stride_t not read): request b's state is row slots[b] of the fp32 pool
+ * state [S, D], updated in place (slots NULL: row b).  A negative slot is a
+ * request that is not there: its output row is zeros.  A slot of S or more
+ * does the same and is reported as LRSCAN_EINVAL by lrscan_sync_check.  Two
+ * requests must not share a slot.
+ */
+int lrscan_step_gates(const lrscan_rows *r, const lrscan_rows *i, const lrscan_rows *x,
+                      const float *lam, float c, float *state, const int32_t *slots, const lrscan_rows *out,
+                      int64_t B, int64_t S, int64_t D, int dtype, void *stream);
+
+/*
  * Whole-sequence affine summary of every lane (the chunk summary of
  * triton_training_scan.py, _real_chunk_summary and its reverse mirror, with
  * one chunk spanning all T steps).  With a'_t = 0 where segment_pos[b,t] == 0

@@ -1,0 +1,173 @@
+// Launchers of the gated-recurrence kernels, the single-token kernel and the
+// reduction of the lam gradient.
+#include "gates_args.h"
+#include "gates_kernels.cuh"
+#include "launch.h"
+
+namespace lrscan {
+namespace {
+
+constexpr int kMaxDev = 64;
+
+template <class St> struct FwdShape;
+template <> struct FwdShape<float> { static constexpr int NW = 8, L = 8, S = 2, CTAS = 2; };
+template <> struct FwdShape<bf16_t> { static constexpr int NW = 8, L = 8, S = 4, CTAS = 2; };
+template <class St> struct BwdShape;
+template <> struct BwdShape<float> { static constexpr int NW = 16, L = 4, S = 2, CTAS = 1; };
+template <> struct BwdShape<bf16_t> { static constexpr int NW = 16, L = 4, S = 4, CTAS = 1; };
+
+// CTAs of `kern` that fit on an SM (asked once per device), its shared memory allowed.
+template <class Kern> int resident(Kern kern, int threads, int smem, int (&cache)[kMaxDev], int *dev_out) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+    if (cache[dev] == 0) {
+        int n = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess)
+            return 0;
+        cache[dev] = n;
+    }
+    *dev_out = dev;
+    return cache[dev];
+}
+
+template <class St, bool BULK, bool SEG> int fwd(const GatesLaunch &L, int sm_count) {
+    using Sh = FwdShape<St>;
+    using Geo = GatesGeo<St, Sh::NW, Sh::L, Sh::S, 3, BULK>;
+    static int cache[kMaxDev] = {};
+    auto kern = gates_fwd_kernel<St, Sh::NW, Sh::L, Sh::S, BULK, SEG, Sh::CTAS>;
+    int dev = 0;
+    const int fit = resident(kern, Geo::kThreads, Geo::kBytes, cache, &dev);
+    if (fit == 0) return 1;
+    const long long tiles = static_cast<long long>(L.a.nl) * L.a.nc, most = static_cast<long long>(fit) * sm_count;
+    kern<<<static_cast<unsigned>(tiles < most ? tiles : most), Geo::kThreads, Geo::kBytes, L.stream>>>(
+        L.a, L.maps[0], L.maps[1], L.maps[2]);
+    return cudaGetLastError() != cudaSuccess;
+}
+
+template <class St, bool BULK, bool SEG> int bwd(const GatesLaunch &L, int sm_count) {
+    using Sh = BwdShape<St>;
+    using Geo = GatesGeo<St, Sh::NW, Sh::L, Sh::S, 4, BULK>;
+    static int cache[kMaxDev] = {};
+    auto kern = gates_bwd_kernel<St, Sh::NW, Sh::L, Sh::S, BULK, SEG, Sh::CTAS>;
+    int dev = 0;
+    const int fit = resident(kern, Geo::kThreads, Geo::kBytes, cache, &dev);
+    if (fit == 0) return 1;
+    const long long tiles = static_cast<long long>(L.a.nl) * L.a.nc, most = static_cast<long long>(fit) * sm_count;
+    kern<<<static_cast<unsigned>(tiles < most ? tiles : most), Geo::kThreads, Geo::kBytes, L.stream>>>(
+        L.a, L.maps[0], L.maps[1], L.maps[2], L.maps[3]);
+    return cudaGetLastError() != cudaSuccess;
+}
+
+template <class St> int pick(const GatesLaunch &L, int dir, int sm_count) {
+    const bool seg = L.a.seg != nullptr;
+    if (dir == 0) {
+        if (L.bulk) return seg ? fwd<St, true, true>(L, sm_count) : fwd<St, true, false>(L, sm_count);
+        return seg ? fwd<St, false, true>(L, sm_count) : fwd<St, false, false>(L, sm_count);
+    }
+    if (L.bulk) return seg ? bwd<St, true, true>(L, sm_count) : bwd<St, true, false>(L, sm_count);
+    return seg ? bwd<St, false, true>(L, sm_count) : bwd<St, false, false>(L, sm_count);
+}
+
+// Column sums of part [rows][D] in a fixed order: a CTA takes 32 columns, its
+// 32 warps take every 32nd row of its slice of rows, and their sums are added
+// in warp order.  lam given: scaled to the gradient of lam.
+__global__ void __launch_bounds__(1024) gates_columns_kernel(const float *part, long long rows, long long D,
+                                                             const float *lam, float *out) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long d = static_cast<long long>(blockIdx.x) * 32 + lane;
+    const long long per = (rows + gridDim.y - 1) / gridDim.y;
+    const long long r0 = per * blockIdx.y, r1 = r0 + per < rows ? r0 + per : rows;
+    float sum = 0.0f;
+    if (d < D) {
+#pragma unroll 8
+        for (long long r = r0 + warp; r < r1; r += 32) sum += __ldg(part + r * D + d);
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && d < D) {
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) sum += sums[w][lane];
+        if (lam != nullptr) {
+            // sigmoid(lam) / softplus(lam); 1 where both are under the least number
+            const float x = lam[d], sp = gate_rate(x, 1.0f);
+            sum *= sp > 0.0f || sp != sp ? (1.0f / (1.0f + expf(-x))) / sp : 1.0f;
+        }
+        out[static_cast<long long>(blockIdx.y) * D + d] = sum;
+    }
+}
+
+// One token of each of B requests; the state's row is the request's slot.
+template <class St> __global__ void __launch_bounds__(256) gates_step_kernel(const GatesStep g) {
+    const long long d = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    if (d >= g.D) return;
+    const float k = gate_rate(__ldg(g.lam + d), g.c);
+    for (long long b = blockIdx.y; b < g.B; b += gridDim.y) {
+        const long long slot = g.slots ? __ldg(g.slots + b) : b;
+        St *out = static_cast<St *>(g.out) + b * g.so + d;
+        float y[1] = {0.0f};
+        if (slot >= 0 && slot < g.S) {
+            float r[2] = {load_one(static_cast<const St *>(g.r) + b * g.sr + d, true), 0.0f};
+            float i[2] = {load_one(static_cast<const St *>(g.i) + b * g.si + d, true), 0.0f};
+            const float x = load_one(static_cast<const St *>(g.x) + b * g.sx + d, true);
+            float *h = g.state + slot * g.D + d;
+            const float before = *h;
+            float rg[2], ig[2], G[2], a[2], s[2], rs[2];
+            const float kk[2] = {k, 0.0f};
+            sigmoid2(rg, r);
+            sigmoid2(ig, i);
+            decay2(kk, rg, true, G, a, s, rs);
+            y[0] = __fmaf_rn(a[0], before, s[0] * (ig[0] * x));
+            *h = y[0];
+        } else if (slot >= g.S && threadIdx.x == 0 && blockIdx.x == 0) {
+            if (atomicCAS(&g.status->code, 0, kErrRange) == 0) {
+                g.status->where = kSiteGatesSlot;
+                g.status->block = static_cast<unsigned>(b);
+            }
+        }
+        store_lanes<St, 1>(out, y);
+    }
+}
+
+}  // namespace
+
+int gates_tile_rows(int dtype, int dir) {
+    if (dir == 0) return dtype == 0 ? FwdShape<float>::NW * FwdShape<float>::L : FwdShape<bf16_t>::NW * FwdShape<bf16_t>::L;
+    return kGatesSave;
+}
+
+int gates_launch(const GatesLaunch &L, int dtype, int dir, int sm_count) {
+    return dtype == 0 ? pick<float>(L, dir, sm_count) : pick<bf16_t>(L, dir, sm_count);
+}
+
+int gates_finish_splits(long long rows) {
+    const long long s = rows / 256;
+    return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+int gates_finish_launch(float *part, long long rows, long long D, const float *lam, float *grad_lam,
+                        cudaStream_t stream) {
+    const int splits = gates_finish_splits(rows);
+    const dim3 grid(static_cast<unsigned>((D + 31) / 32), static_cast<unsigned>(splits));
+    if (splits == 1) {
+        gates_columns_kernel<<<grid, 1024, 0, stream>>>(part, rows, D, lam, grad_lam);
+    } else {
+        float *second = part + rows * D;
+        gates_columns_kernel<<<grid, 1024, 0, stream>>>(part, rows, D, nullptr, second);
+        gates_columns_kernel<<<dim3(grid.x, 1), 1024, 0, stream>>>(second, splits, D, lam, grad_lam);
+    }
+    return cudaGetLastError() != cudaSuccess;
+}
+
+int gates_step_launch(const GatesStep &L, int dtype) {
+    const dim3 grid(static_cast<unsigned>((L.D + 255) / 256), static_cast<unsigned>(L.B < 65535 ? L.B : 65535));
+    if (dtype == 0)
+        gates_step_kernel<float><<<grid, 256, 0, L.stream>>>(L);
+    else
+        gates_step_kernel<bf16_t><<<grid, 256, 0, L.stream>>>(L);
+    return cudaGetLastError() != cudaSuccess;
+}
+
+}  // namespace lrscan

@@ -9,6 +9,7 @@
 
 #include <mutex>
 
+#include "lrscan.h"
 #include "state_args.h"
 #include "stream_args.h"
 
@@ -165,6 +166,26 @@ int selftest_wait_launch(DevStatus *status, uint64_t timeout_ns, cudaStream_t st
 
 // Records the detail text lrscan_last_error() returns and passes code through.
 int report_error(int code, const char *msg);
+
+// What the entry points outside lrscan_abi.cu take from it: a call's checks,
+// device, stream and workspace, by the same rules as the scan's own calls.
+struct CallCtx {
+    int device;
+    int sm_count;
+    DevStatus *status;
+    uint64_t timeout_ns;
+    void *dev;  // the library's record of the device
+};
+void begin_call();  // clears the thread's last error
+int report_errorf(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+int call_shape(int64_t B, int64_t T, int64_t D, int dtype);
+int call_device(CallCtx *out);
+cudaStream_t call_stream(void *stream);
+int call_workspace(const CallCtx &ctx, cudaStream_t st, size_t need, const ::lrscan_opts *opts, void **ws);
+int call_copy_or_zero(float *dst, const float *src, int64_t B, int64_t D, cudaStream_t st);
+// Tensor map of rows with strides (elements) of a batch row and a token; box dt lanes, w tokens.
+int encode_rows_map(CUtensorMap *m, const void *ptr, int64_t stride_b, int64_t stride_t, int dtype, int64_t B, int64_t T,
+                    int64_t D, int dt, int w);
 // Reads and clears the device status word after `st` drains (lrscan_abi.cu).
 int take_device_status(cudaStream_t st);
 

@@ -528,20 +528,7 @@ void fill_info(const Choice &c, lrscan_plan_info *info) {
 // Tensor maps: a [B][T][D] tensor viewed as 3-D {D, T, B}; box {DT, W, 1}.
 // -------------------------------------------------------------------------
 int encode_map(CUtensorMap *m, const void *ptr, int dtype, int64_t B, int64_t T, int64_t D, int dt, int w) {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * esize(dtype),
-                                   static_cast<cuuint64_t>(T) * static_cast<cuuint64_t>(D) * esize(dtype)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(dt), static_cast<cuuint32_t>(w), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(m, dtype == LRSCAN_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                          3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        return fail(LRSCAN_EINVAL, "cuTensorMapEncodeTiled failed (%d) for ptr %p dims {%lld,%lld,%lld} box {%d,%d}",
-                    static_cast<int>(r), ptr, static_cast<long long>(D), static_cast<long long>(T),
-                    static_cast<long long>(B), dt, w);
-    return LRSCAN_OK;
+    return encode_rows_map(m, ptr, T * D, D, dtype, B, T, D, dt, w);
 }
 
 int check_shape(int64_t B, int64_t T, int64_t D, int dtype) {
@@ -1420,6 +1407,50 @@ int run_gbwd(const float *eta, const float *nu_log, const void *out, const void 
 
 // Lets other translation units of the library report why a call failed.
 int report_error(int code, const char *msg) { return fail(code, "%s", msg); }
+int report_errorf(int code, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    std::vsnprintf(t_detail, sizeof t_detail, fmt, ap);
+    va_end(ap);
+    return code;
+}
+void begin_call() { t_detail[0] = 0; }
+int call_shape(int64_t B, int64_t T, int64_t D, int dtype) { return check_shape(B, T, D, dtype); }
+int call_device(CallCtx *out) {
+    DeviceCtx *c = nullptr;
+    const int rc = device_ctx(&c);
+    if (rc) return rc;
+    out->device = static_cast<int>(c - g_dev);
+    out->sm_count = c->sm_count;
+    out->status = c->status;
+    out->timeout_ns = g_timeout_ns.load();
+    out->dev = c;
+    return LRSCAN_OK;
+}
+cudaStream_t call_stream(void *stream) { return pick_stream(stream); }
+int call_workspace(const CallCtx &ctx, cudaStream_t st, size_t need, const lrscan_opts *opts, void **ws) {
+    return workspace_for(static_cast<DeviceCtx *>(ctx.dev), st, need, opts, ws);
+}
+int call_copy_or_zero(float *dst, const float *src, int64_t B, int64_t D, cudaStream_t st) {
+    return copy_or_zero(dst, src, B, D, st);
+}
+int encode_rows_map(CUtensorMap *m, const void *ptr, int64_t stride_b, int64_t stride_t, int dtype, int64_t B, int64_t T,
+                    int64_t D, int dt, int w) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride_t) * esize(dtype),
+                                   static_cast<cuuint64_t>(stride_b) * esize(dtype)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(dt), static_cast<cuuint32_t>(w), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, dtype == LRSCAN_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(LRSCAN_EINVAL, "cuTensorMapEncodeTiled failed (%d) for ptr %p dims {%lld,%lld,%lld} box {%d,%d}",
+                    static_cast<int>(r), ptr, static_cast<long long>(D), static_cast<long long>(T),
+                    static_cast<long long>(B), dt, w);
+    return LRSCAN_OK;
+}
 
 // After `st` has drained: the first error a kernel recorded on the current
 // device since the last check (cleared), else LRSCAN_OK.

@@ -844,3 +844,14 @@ def gated_scan(eta, nu_log, b, path=None):
     """Differentiable scan whose decays exp(-exp(nu_log[d]) * exp(eta[b, t])) are
     generated in the kernel; returns out [B, T, D]."""
     return GatedScan.apply(eta, nu_log, b, path)
+
+
+# the operators around the scan (module layer), reached from here like the rest
+from .layer import (  # noqa: E402,F401
+    GateScan,
+    gate_scan,
+    lrscan_bwd_gates,
+    lrscan_fwd_gates,
+    lrscan_gates_workspace_bytes,
+    lrscan_step_gates,
+)

@@ -1,0 +1,114 @@
+"""The gated recurrence in 64 bits, token by token, with bounds on what 32-bit
+arithmetic may be off by.
+
+Bounds (u = 2^-24, one fp32 rounding is off by at most u relative):
+a gate is an exponential, a sum and a reciprocal (2^-22 + u + 2^-23 relative at
+most, under 8u), the rate k under 8u, so the exponent G is within 17u of itself
+and a = exp(-G) within 17u G + 8u of itself; s = sqrt(1 - a^2) comes from 1 - a,
+itself within 26u where G is small, and is within 24u of itself.  Hence a step of
+the recurrence adds at most EA u |a h| + EB u |b| to the state's error, where
+EA = 34 covers 17 G (G <= 1 wherever a is not negligible; G exp(-G) <= 1/e) + 8 +
+two roundings of the maps' regrouping, and EB = 64 covers s ig x and their
+products.  The same recurrence bounds the adjoint.
+"""
+import torch
+
+U = 2.0 ** -24
+EA, EB = 34.0, 64.0
+FLUSH = 2.0 ** -62
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu()
+
+
+def gates(r, i, lam, c, seg):
+    rg, ig = torch.sigmoid(r), torch.sigmoid(i)
+    sp = torch.nn.functional.softplus(lam, threshold=1e9)
+    G = c * sp * rg
+    a = torch.exp(-G)
+    m2 = -torch.expm1(-2 * G)
+    if seg is not None:
+        first = (seg == 0)[..., None]
+        a, m2 = torch.where(first, 0.0, a), torch.where(first, 1.0, m2)
+    return rg, ig, G, a, m2.clamp(min=0).sqrt()
+
+
+def walk(a, b, h, err, ix):
+    """States of h_t = a_t h_{t-1} + b_t, b = s ix, and their error bounds,
+    [B, T, D]; a token with a = 0 takes nothing of the state before it."""
+    out, bound = torch.empty_like(b), torch.empty_like(b)
+    for t in range(b.shape[1]):
+        first = a[:, t] == 0
+        ah = torch.where(first, 0.0, a[:, t] * h)
+        err = torch.where(first, 0.0, a[:, t] * err) + U * (EA * ah.abs() + EB * b[:, t].abs()) + FLUSH * ix[:, t].abs()
+        h = ah + b[:, t]
+        out[:, t], bound[:, t] = h, err
+    return out, bound, h, err
+
+
+def forward(r, i, x, lam, c=8.0, h0=None, seg=None):
+    """(out, last) and their bounds."""
+    r, i, x, lam = f64(r), f64(i), f64(x), f64(lam)
+    seg = None if seg is None else seg.cpu()
+    B, T, D = x.shape
+    h = torch.zeros((B, D), dtype=torch.float64) if h0 is None else f64(h0)
+    rg, ig, G, a, s = gates(r, i, lam, c, seg)
+    out, bound, last, elast = walk(a, s * ig * x, h, torch.zeros_like(h), ig * x)
+    return out, last, bound, elast
+
+
+def backward(r, i, x, lam, grad_out, c=8.0, h0=None, seg=None, grad_last=None):
+    """{name: (gradient, bound)}"""
+    out, _, eh, _ = forward(r, i, x, lam, c, h0, seg)
+    r, i, x, lam, go = f64(r), f64(i), f64(x), f64(lam), f64(grad_out)
+    seg = None if seg is None else seg.cpu()
+    B, T, D = x.shape
+    h0 = torch.zeros((B, D), dtype=torch.float64) if h0 is None else f64(h0)
+    rg, ig, G, a, s = gates(r, i, lam, c, seg)
+    prev = torch.cat([h0[:, None], out[:, :-1]], 1)
+    eprev = torch.cat([torch.zeros_like(h0)[:, None], eh[:, :-1]], 1)
+    cc = torch.zeros_like(h0) if grad_last is None else f64(grad_last)
+    ec = torch.zeros_like(cc)
+    g, eg = torch.empty_like(go), torch.empty_like(go)
+    for t in range(T - 1, -1, -1):
+        g[:, t] = go[:, t] + cc
+        eg[:, t] = ec + 2 * U * (go[:, t].abs() + cc.abs())
+        cc = a[:, t] * g[:, t]
+        ec = a[:, t] * eg[:, t] + U * EA * cc.abs()
+    live = a > 0
+    over = torch.where(live, ig * x * a / s, 0.0)        # ig x a / s
+    over = torch.where(torch.isfinite(over), over, 0.0)  # G = 0: times G it is 0
+    mult = torch.where(live, G * a, 0.0)
+    q = mult * g * (over - torch.where(live, prev, 0.0))
+    eq = mult * (eg * (over - prev).abs() + g.abs() * (eprev + EB * U * (over.abs() + prev.abs()))) + EB * U * q.abs() + FLUSH * (g * ig * x).abs()
+    eq = torch.where(live, eq, 0.0)
+    sp = torch.nn.functional.softplus(lam, threshold=1e9)
+    ratio = torch.where(sp > 0, torch.sigmoid(lam) / sp, 1.0)
+    gx = g * s * ig
+    egx = eg * s * ig + EB * U * gx.abs() + FLUSH * (g * ig).abs()
+    gi = gx * x * (1 - ig)
+    # 1 - gate is off by the gate's own error, not by a part of itself
+    egi = egx * (x * (1 - ig)).abs() + EB * U * (gx * x).abs()
+    gr, egr = q * (1 - rg), eq * (1 - rg) + EB * U * q.abs()
+    n = B * T
+    glam = ratio * q.sum((0, 1))
+    eglam = ratio * (eq.sum((0, 1)) + U * (EB + n ** 0.5) * q.abs().sum((0, 1)))
+    return {"grad_r": (gr, egr), "grad_i": (gi, egi), "grad_x": (gx, egx), "grad_lam": (glam, eglam),
+            "grad_h0": (cc, ec)}
+
+
+def assert_within(got, ref, bound, dtype, what):
+    """|got - ref| <= bound, and the storage type's rounding (2^-8 of the value
+    at most in bf16, whose significand has 8 bits; 2^-24 in fp32; 1e-37 covers
+    what is flushed to zero)."""
+    got = got.detach().double().cpu()
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    allowed = bound + half * (ref.abs() + bound) + 1e-37
+    finite = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), f"{what}: NaN in other places"
+    assert torch.equal(got[~finite & ~torch.isnan(ref)], ref[~finite & ~torch.isnan(ref)]), f"{what}: infinities differ"
+    off = ((got - ref).abs() - allowed)[finite]
+    assert off.numel() == 0 or off.max() <= 0, (
+        f"{what}: off by {(got - ref).abs()[finite].max():.3g} at most, "
+        f"{int((off > 0).sum())} of {off.numel()} over the bound, by {off.max():.3g}")
