@@ -456,6 +456,60 @@ int lrscan_step_gates(const lrscan_rows *r, const lrscan_rows *i, const lrscan_r
                       int64_t B, int64_t S, int64_t D, int dtype, void *stream);
 
 /*
+ * Short causal convolution of each channel, which such layers run in front of
+ * their recurrence.  x: [B, T, D] in the storage dtype; w: fp32 [D, K], K = 2
+ * to 8 taps, w[d, K-1] the newest token's; bias: fp32 [D] or NULL;
+ *   forward   out_t = bias + sum_{k<K} w[K-1-k] x_{t-k}
+ * where a tap counts only if segment_pos (int32 [B, T] or NULL) is 0 at none
+ * of t-k+1 .. t, and tokens before token 0 are x0 (storage dtype [B, K-1, D],
+ * oldest first) or zeros.  last (storage dtype [B, K-1, D], optional): the
+ * last K-1 tokens of x0 and x, restarts or not; the next call's x0.
+ *   backward  for sum grad_out * out + sum grad_last * last: grad_x, grad_w
+ * (fp32 [D, K]), grad_bias (fp32 [D] or NULL), grad_x0 ([B, K-1, D] or NULL);
+ * sums are fp32 in a fixed order.  Scratch of lrscan_conv_workspace_bytes
+ * bytes: library-owned per (device, stream), or opts->workspace.
+ * With T == 0 the forward copies x0 (or zeros) into last, the backward writes
+ * zeros and copies grad_last (or zeros) into grad_x0.
+ */
+int lrscan_fwd_conv(const lrscan_rows *x, const float *w, const float *bias, int K, const void *x0,
+                    const int32_t *segment_pos, const lrscan_rows *out, void *last,
+                    int64_t B, int64_t T, int64_t D, int dtype, void *stream);
+int lrscan_bwd_conv(const lrscan_rows *x, const float *w, int K, const void *x0, const int32_t *segment_pos,
+                    const lrscan_rows *grad_out, const void *grad_last, const lrscan_rows *grad_x,
+                    float *grad_w, float *grad_bias, void *grad_x0,
+                    int64_t B, int64_t T, int64_t D, int dtype, void *stream, const lrscan_opts *opts);
+size_t lrscan_conv_workspace_bytes(int64_t B, int64_t T, int64_t D, int K);
+/* One token of each of B requests on a pool of windows state [S, K-1, D]
+ * (storage dtype, oldest first), updated in place; slots as
+ * lrscan_step_gates. */
+int lrscan_step_conv(const lrscan_rows *x, const float *w, const float *bias, int K, void *state,
+                     const int32_t *slots, const lrscan_rows *out,
+                     int64_t B, int64_t S, int64_t D, int dtype, void *stream);
+
+/*
+ * Token embedding with scaling.  ids: N token ids, int32 or int64 (id_bytes 4
+ * or 8); weight: [V, D]; out: [N, D]; each of dtype LRSCAN_F32 or LRSCAN_BF16
+ * on its own (wdtype, odtype; gdtype for grad_out).
+ *   forward   out[n] = scale * weight[ids[n]], one fp32 product, rounded once
+ *   backward  grad_weight[v] = scale * sum of grad_out[n] over ids[n] = v, the
+ *             sum in fp32 and in the same order on every call; accumulate != 0
+ *             adds it to what grad_weight holds, else rows without a token are
+ *             zeros
+ * A negative id is no token: a row of zeros, and no gradient.  An id of V or
+ * more does the same and is reported as LRSCAN_EINVAL by lrscan_sync_check.
+ * All tensors are contiguous.  Rows of a multiple of eight lanes on 16-byte
+ * boundaries take wide accesses.  Backward scratch of
+ * lrscan_embed_workspace_bytes bytes: library-owned per (device, stream), or
+ * opts->workspace.
+ */
+int lrscan_fwd_embed(const void *ids, int id_bytes, const void *weight, int wdtype, float scale,
+                     void *out, int odtype, int64_t N, int64_t V, int64_t D, void *stream);
+int lrscan_bwd_embed(const void *ids, int id_bytes, const void *grad_out, int gdtype, float scale,
+                     void *grad_weight, int wdtype, int accumulate,
+                     int64_t N, int64_t V, int64_t D, void *stream, const lrscan_opts *opts);
+size_t lrscan_embed_workspace_bytes(int64_t N, int64_t V, int64_t D);
+
+/*
  * Whole-sequence affine summary of every lane (the chunk summary of
  * triton_training_scan.py, _real_chunk_summary and its reverse mirror, with
  * one chunk spanning all T steps).  With a'_t = 0 where segment_pos[b,t] == 0

@@ -1,0 +1,50 @@
+// Arguments of the causal-convolution kernels (conv_kernels.cuh).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gates_args.h"
+
+namespace lrscan {
+
+constexpr int kConvMinTaps = 2, kConvMaxTaps = 8;
+constexpr int kConvSteps = 32;  // tokens a thread walks
+constexpr int kConvSplit = 8;   // walks of a CTA, one after another in time
+
+struct ConvArgs {
+    RowsArg x, o;             // o: forward out, backward grad_x
+    RowsArg go;               // backward: grad_out
+    const float *w, *bias;    // [D, K], [D] or null
+    const void *x0;           // [B, K-1, D] or null: the tokens before token 0
+    const int32_t *seg;       // [B, T] or null
+    void *last;               // forward, [B, K-1, D] or null: the last tokens of x0 and x
+    const void *grad_last;    // backward, [B, K-1, D] or null
+    void *grad_x0;            // backward, [B, K-1, D] or null
+    float *part;              // backward: [B * chunks][K + 1][D]
+    long long B, T, D;
+    unsigned chunks, ndt;     // CTAs in time, and over the lanes
+    bool vec;                 // rows fit accesses of four lanes
+    cudaStream_t stream;
+};
+int conv_fwd_launch(const ConvArgs &a, int K, int dtype);
+int conv_bwd_launch(const ConvArgs &a, int K, int dtype);
+int conv_finish_slices(long long rows);
+int conv_finish_launch(float *part, long long rows, long long D, int K, float *grad_w, float *grad_bias,
+                       cudaStream_t stream);
+
+// One token a row: window state [S, K-1, D] in place; slots may be null.
+struct ConvStep {
+    const void *x;
+    long long sx, so;
+    void *out;
+    const float *w, *bias;
+    void *state;
+    const int32_t *slots;
+    long long S, B, D;
+    DevStatus *status;
+    cudaStream_t stream;
+};
+int conv_step_launch(const ConvStep &a, int K, int dtype);
+
+}  // namespace lrscan

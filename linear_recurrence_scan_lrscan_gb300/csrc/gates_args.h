@@ -57,8 +57,8 @@ struct GatesLaunch {
 int gates_tile_rows(int dtype, int dir);
 int gates_launch(const GatesLaunch &L, int dtype, int dir, int sm_count);
 // grad_lam from the partial sums part [rows][D], in a fixed order; `part` has
-// gates_finish_splits(rows) more rows after them.
-int gates_finish_splits(long long rows);
+// gates_finish_slices(rows) more rows after them.
+int gates_finish_slices(long long rows);
 int gates_finish_launch(float *part, long long rows, long long D, const float *lam, float *grad_lam,
                         cudaStream_t stream);
 // One token a row: state [S, D] in place; slots may be null.

@@ -1,0 +1,96 @@
+// Launchers of the causal-convolution kernels.
+#include "column_sums.cuh"
+#include "conv_args.h"
+#include "conv_kernels.cuh"
+#include "launch.h"
+
+namespace lrscan {
+namespace {
+
+struct PutTaps {
+    float *gw, *gb;
+    long long D;
+    int K;
+    __device__ void operator()(long long, long long col, float sum) const {
+        const long long k = col / D, d = col % D;
+        if (k < K)
+            gw[d * K + k] = sum;
+        else if (gb != nullptr)
+            gb[d] = sum;
+    }
+};
+
+template <class St, int V, int K> int run(const ConvArgs &a, int dir) {
+    const dim3 block(32, kConvSplit);
+    for (long long b0 = 0; b0 < a.B; b0 += 65535) {
+        ConvArgs s = a;
+        s.ndt = static_cast<unsigned>((a.D + 32 * V - 1) / (32 * V));
+        const long long off = b0 * (K - 1) * a.D * static_cast<long long>(sizeof(St));
+        s.B = a.B - b0 < 65535 ? a.B - b0 : 65535;
+        for (RowsArg *r : {&s.x, &s.o, &s.go})
+            if (r->p) r->p = static_cast<St *>(r->p) + b0 * r->sb;
+        if (a.seg) s.seg = a.seg + b0 * a.T;
+        if (a.x0) s.x0 = static_cast<const char *>(a.x0) + off;
+        if (a.last) s.last = static_cast<char *>(a.last) + off;
+        if (a.grad_last) s.grad_last = static_cast<const char *>(a.grad_last) + off;
+        if (a.grad_x0) s.grad_x0 = static_cast<char *>(a.grad_x0) + off;
+        if (a.part) s.part = a.part + b0 * a.chunks * (K + 1) * a.D;
+        const dim3 grid(s.ndt * a.chunks, static_cast<unsigned>(s.B));
+        if (dir == 0)
+            conv_fwd_kernel<St, V, K><<<grid, block, 0, a.stream>>>(s);
+        else
+            conv_bwd_kernel<St, V, K><<<grid, block, 0, a.stream>>>(s);
+        if (cudaGetLastError() != cudaSuccess) return 1;
+    }
+    return 0;
+}
+
+template <class St, int V> int taps(const ConvArgs &a, int K, int dir) {
+    switch (K) {
+        case 2: return run<St, V, 2>(a, dir);
+        case 3: return run<St, V, 3>(a, dir);
+        case 4: return run<St, V, 4>(a, dir);
+        case 5: return run<St, V, 5>(a, dir);
+        case 6: return run<St, V, 6>(a, dir);
+        case 7: return run<St, V, 7>(a, dir);
+        case 8: return run<St, V, 8>(a, dir);
+        default: return 1;
+    }
+}
+
+int pick(const ConvArgs &a, int K, int dtype, int dir) {
+    if (dtype == 0) return a.vec ? taps<float, 4>(a, K, dir) : taps<float, 1>(a, K, dir);
+    return a.vec ? taps<bf16_t, 4>(a, K, dir) : taps<bf16_t, 1>(a, K, dir);
+}
+
+template <class St, int K> void step(const ConvStep &a, dim3 grid) { conv_step_kernel<St, K><<<grid, 256, 0, a.stream>>>(a); }
+
+template <class St> int step_taps(const ConvStep &a, int K, dim3 grid) {
+    switch (K) {
+        case 2: step<St, 2>(a, grid); break;
+        case 3: step<St, 3>(a, grid); break;
+        case 4: step<St, 4>(a, grid); break;
+        case 5: step<St, 5>(a, grid); break;
+        case 6: step<St, 6>(a, grid); break;
+        case 7: step<St, 7>(a, grid); break;
+        case 8: step<St, 8>(a, grid); break;
+        default: return 1;
+    }
+    return cudaGetLastError() != cudaSuccess;
+}
+
+}  // namespace
+
+int conv_fwd_launch(const ConvArgs &a, int K, int dtype) { return pick(a, K, dtype, 0); }
+int conv_bwd_launch(const ConvArgs &a, int K, int dtype) { return pick(a, K, dtype, 1); }
+int conv_finish_slices(long long rows) { return column_slices(rows); }
+int conv_finish_launch(float *part, long long rows, long long D, int K, float *grad_w, float *grad_bias,
+                       cudaStream_t stream) {
+    return column_sums(part, rows, (K + 1) * D, PutTaps{grad_w, grad_bias, D, K}, stream);
+}
+int conv_step_launch(const ConvStep &a, int K, int dtype) {
+    const dim3 grid(static_cast<unsigned>((a.D + 255) / 256), static_cast<unsigned>(a.B < 65535 ? a.B : 65535));
+    return dtype == 0 ? step_taps<float>(a, K, grid) : step_taps<bf16_t>(a, K, grid);
+}
+
+}  // namespace lrscan

@@ -1,5 +1,6 @@
 // Launchers of the gated-recurrence kernels, the single-token kernel and the
 // reduction of the lam gradient.
+#include "column_sums.cuh"
 #include "gates_args.h"
 #include "gates_kernels.cuh"
 #include "launch.h"
@@ -69,35 +70,16 @@ template <class St> int pick(const GatesLaunch &L, int dir, int sm_count) {
     return seg ? bwd<St, false, true>(L, sm_count) : bwd<St, false, false>(L, sm_count);
 }
 
-// Column sums of part [rows][D] in a fixed order: a CTA takes 32 columns, its
-// 32 warps take every 32nd row of its slice of rows, and their sums are added
-// in warp order.  lam given: scaled to the gradient of lam.
-__global__ void __launch_bounds__(1024) gates_columns_kernel(const float *part, long long rows, long long D,
-                                                             const float *lam, float *out) {
-    __shared__ float sums[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long d = static_cast<long long>(blockIdx.x) * 32 + lane;
-    const long long per = (rows + gridDim.y - 1) / gridDim.y;
-    const long long r0 = per * blockIdx.y, r1 = r0 + per < rows ? r0 + per : rows;
-    float sum = 0.0f;
-    if (d < D) {
-#pragma unroll 8
-        for (long long r = r0 + warp; r < r1; r += 32) sum += __ldg(part + r * D + d);
+// The gradient of lam: sigmoid(lam) / softplus(lam) times the sum (1 where both
+// are under the least number).
+struct PutLam {
+    const float *lam;
+    float *out;
+    __device__ void operator()(long long, long long d, float sum) const {
+        const float x = lam[d], sp = gate_rate(x, 1.0f);
+        out[d] = sp > 0.0f || sp != sp ? sum * ((1.0f / (1.0f + expf(-x))) / sp) : sum;
     }
-    sums[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && d < D) {
-        sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 32; ++w) sum += sums[w][lane];
-        if (lam != nullptr) {
-            // sigmoid(lam) / softplus(lam); 1 where both are under the least number
-            const float x = lam[d], sp = gate_rate(x, 1.0f);
-            sum *= sp > 0.0f || sp != sp ? (1.0f / (1.0f + expf(-x))) / sp : 1.0f;
-        }
-        out[static_cast<long long>(blockIdx.y) * D + d] = sum;
-    }
-}
+};
 
 // One token of each of B requests; the state's row is the request's slot.
 template <class St> __global__ void __launch_bounds__(256) gates_step_kernel(const GatesStep g) {
@@ -142,23 +124,11 @@ int gates_launch(const GatesLaunch &L, int dtype, int dir, int sm_count) {
     return dtype == 0 ? pick<float>(L, dir, sm_count) : pick<bf16_t>(L, dir, sm_count);
 }
 
-int gates_finish_splits(long long rows) {
-    const long long s = rows / 256;
-    return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
-}
+int gates_finish_slices(long long rows) { return column_slices(rows); }
 
 int gates_finish_launch(float *part, long long rows, long long D, const float *lam, float *grad_lam,
                         cudaStream_t stream) {
-    const int splits = gates_finish_splits(rows);
-    const dim3 grid(static_cast<unsigned>((D + 31) / 32), static_cast<unsigned>(splits));
-    if (splits == 1) {
-        gates_columns_kernel<<<grid, 1024, 0, stream>>>(part, rows, D, lam, grad_lam);
-    } else {
-        float *second = part + rows * D;
-        gates_columns_kernel<<<grid, 1024, 0, stream>>>(part, rows, D, nullptr, second);
-        gates_columns_kernel<<<dim3(grid.x, 1), 1024, 0, stream>>>(second, splits, D, lam, grad_lam);
-    }
-    return cudaGetLastError() != cudaSuccess;
+    return column_sums(part, rows, D, PutLam{lam, grad_lam}, stream);
 }
 
 int gates_step_launch(const GatesStep &L, int dtype) {

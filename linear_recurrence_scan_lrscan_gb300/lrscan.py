@@ -848,10 +848,21 @@ def gated_scan(eta, nu_log, b, path=None):
 
 # the operators around the scan (module layer), reached from here like the rest
 from .layer import (  # noqa: E402,F401
+    CausalConv,
+    Embed,
     GateScan,
+    causal_conv,
+    embed,
     gate_scan,
+    lrscan_bwd_conv,
+    lrscan_bwd_embed,
     lrscan_bwd_gates,
+    lrscan_conv_workspace_bytes,
+    lrscan_embed_workspace_bytes,
+    lrscan_fwd_conv,
+    lrscan_fwd_embed,
     lrscan_fwd_gates,
     lrscan_gates_workspace_bytes,
+    lrscan_step_conv,
     lrscan_step_gates,
 )
