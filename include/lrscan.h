@@ -418,8 +418,8 @@ typedef struct lrscan_rows {
  *             ig, grad_i = grad_x x (1 - ig), grad_lam = sigmoid(lam) /
  *             softplus(lam) sum_{b,t} q (fp32 [D]), grad_h0 = a_0 g_0
  *
- * State, maps and sums are fp32.  saved (fp32 [B, ceil(T/64), D], optional):
- * the state before tokens 0, 64, 128, ..., from which the backward makes the
+ * State, maps and sums are fp32.  saved (fp32 [B, ceil(T/16), D], optional):
+ * the state before tokens 0, 16, 32, ..., from which the backward makes the
  * states again, so it reads no output and no rounding of one; the backward
  * needs it, and takes h0 from its first row (state->h0 is not read).  The
  * logistic functions, the decay and the square root are accurate to a few

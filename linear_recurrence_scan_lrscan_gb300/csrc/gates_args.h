@@ -20,7 +20,7 @@ struct RowsArg {
     long long sb, st;
 };
 
-constexpr int kGatesSave = 64;    // tokens between saved states
+constexpr int kGatesSave = 16;    // tokens between saved states
 constexpr int kGatesRadix = 16;   // tiles a level of the tree of maps joins
 constexpr int kGatesLanes = 64;   // lanes of a tile
 
@@ -53,8 +53,7 @@ struct GatesLaunch {
     cudaStream_t stream;
 };
 
-// The tile a launch uses: rows (tokens) of a tile.
-int gates_tile_rows(int dtype, int dir);
+constexpr int kGatesTileRows = 64;  // tokens of a tile
 int gates_launch(const GatesLaunch &L, int dtype, int dir, int sm_count);
 // grad_lam from the partial sums part [rows][D], in a fixed order; `part` has
 // gates_finish_slices(rows) more rows after them.

@@ -10,12 +10,12 @@ namespace {
 
 constexpr int kMaxDev = 64;
 
-template <class St> struct FwdShape;
-template <> struct FwdShape<float> { static constexpr int NW = 8, L = 8, S = 2, CTAS = 2; };
-template <> struct FwdShape<bf16_t> { static constexpr int NW = 8, L = 8, S = 4, CTAS = 2; };
-template <class St> struct BwdShape;
-template <> struct BwdShape<float> { static constexpr int NW = 16, L = 4, S = 2, CTAS = 1; };
-template <> struct BwdShape<bf16_t> { static constexpr int NW = 16, L = 4, S = 4, CTAS = 1; };
+// Teams and stages of a CTA: what the registers and 227 KB of shared memory hold.
+template <class St, int DIR> struct Shape;
+template <> struct Shape<float, 0> { static constexpr int teams = 4, stages = 4; };
+template <> struct Shape<float, 1> { static constexpr int teams = 3, stages = 3; };
+template <> struct Shape<bf16_t, 0> { static constexpr int teams = 4, stages = 8; };
+template <> struct Shape<bf16_t, 1> { static constexpr int teams = 4, stages = 6; };
 
 // CTAs of `kern` that fit on an SM (asked once per device), its shared memory allowed.
 template <class Kern> int resident(Kern kern, int threads, int smem, int (&cache)[kMaxDev], int *dev_out) {
@@ -33,10 +33,10 @@ template <class Kern> int resident(Kern kern, int threads, int smem, int (&cache
 }
 
 template <class St, bool BULK, bool SEG> int fwd(const GatesLaunch &L, int sm_count) {
-    using Sh = FwdShape<St>;
-    using Geo = GatesGeo<St, Sh::NW, Sh::L, Sh::S, 3, BULK>;
+    using Sh = Shape<St, 0>;
+    using Geo = GatesGeo<St, Sh::teams, Sh::stages, 3, BULK>;
     static int cache[kMaxDev] = {};
-    auto kern = gates_fwd_kernel<St, Sh::NW, Sh::L, Sh::S, BULK, SEG, Sh::CTAS>;
+    auto kern = gates_fwd_kernel<St, Sh::teams, Sh::stages, BULK, SEG>;
     int dev = 0;
     const int fit = resident(kern, Geo::kThreads, Geo::kBytes, cache, &dev);
     if (fit == 0) return 1;
@@ -47,10 +47,10 @@ template <class St, bool BULK, bool SEG> int fwd(const GatesLaunch &L, int sm_co
 }
 
 template <class St, bool BULK, bool SEG> int bwd(const GatesLaunch &L, int sm_count) {
-    using Sh = BwdShape<St>;
-    using Geo = GatesGeo<St, Sh::NW, Sh::L, Sh::S, 4, BULK>;
+    using Sh = Shape<St, 1>;
+    using Geo = GatesGeo<St, Sh::teams, Sh::stages, 4, BULK>;
     static int cache[kMaxDev] = {};
-    auto kern = gates_bwd_kernel<St, Sh::NW, Sh::L, Sh::S, BULK, SEG, Sh::CTAS>;
+    auto kern = gates_bwd_kernel<St, Sh::teams, Sh::stages, BULK, SEG>;
     int dev = 0;
     const int fit = resident(kern, Geo::kThreads, Geo::kBytes, cache, &dev);
     if (fit == 0) return 1;
@@ -100,7 +100,7 @@ template <class St> __global__ void __launch_bounds__(256) gates_step_kernel(con
             const float kk[2] = {k, 0.0f};
             sigmoid2(rg, r);
             sigmoid2(ig, i);
-            decay2(kk, rg, true, G, a, s, rs);
+            decay2<true>(kk, rg, G, a, s, rs);
             y[0] = __fmaf_rn(a[0], before, s[0] * (ig[0] * x));
             *h = y[0];
         } else if (slot >= g.S && threadIdx.x == 0 && blockIdx.x == 0) {
@@ -114,11 +114,6 @@ template <class St> __global__ void __launch_bounds__(256) gates_step_kernel(con
 }
 
 }  // namespace
-
-int gates_tile_rows(int dtype, int dir) {
-    if (dir == 0) return dtype == 0 ? FwdShape<float>::NW * FwdShape<float>::L : FwdShape<bf16_t>::NW * FwdShape<bf16_t>::L;
-    return kGatesSave;
-}
 
 int gates_launch(const GatesLaunch &L, int dtype, int dir, int sm_count) {
     return dtype == 0 ? pick<float>(L, dir, sm_count) : pick<bf16_t>(L, dir, sm_count);

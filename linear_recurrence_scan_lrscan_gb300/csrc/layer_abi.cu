@@ -72,9 +72,9 @@ struct GatesScratch {
 };
 // Ticket and published maps (only where tiles follow one another in time),
 // then the backward's partial sums of the lam gradient.
-GatesScratch gates_scratch(int64_t B, int64_t T, int64_t D, int dtype, int dir) {
+GatesScratch gates_scratch(int64_t B, int64_t T, int64_t D, int dir) {
     GatesScratch s{};
-    const int64_t rows = gates_tile_rows(dtype, dir);
+    const int64_t rows = kGatesTileRows;
     s.nl = B * ((D + kGatesLanes - 1) / kGatesLanes);
     s.nc = (T + rows - 1) / rows;
     s.n1 = (s.nc + kGatesRadix - 1) / kGatesRadix;
@@ -118,7 +118,7 @@ int gates_common(GatesLaunch *L, const lrscan_rows *r, const lrscan_rows *i, con
 // Everything after the checks: device, workspace, tensor maps, launch.
 int gates_run(GatesLaunch *L, int dtype, int dir, float *grad_lam, void *stream, const lrscan_opts *opts) {
     const int64_t B = L->a.B, T = L->a.T, D = L->a.D;
-    const GatesScratch sc = gates_scratch(B, T, D, dtype, dir);
+    const GatesScratch sc = gates_scratch(B, T, D, dir);
     if (sc.nl > 0x7fffffffLL || sc.nl * sc.nc > 0x7fffffffLL)
         return report_errorf(LRSCAN_EINVAL, "too many tiles: B %lld, T %lld, D %lld", static_cast<long long>(B),
                              static_cast<long long>(T), static_cast<long long>(D));
@@ -146,7 +146,7 @@ int gates_run(GatesLaunch *L, int dtype, int dir, float *grad_lam, void *stream,
         const RowsArg *in[4] = {&a.r, &a.i, &a.x, &a.go};
         for (int k = 0; k < (dir ? 4 : 3); ++k)
             if ((rc = encode_rows_map(&L->maps[k], in[k]->p, in[k]->sb, in[k]->st, dtype, B, T, D, kGatesLanes,
-                                      gates_tile_rows(dtype, dir))))
+                                      kGatesTileRows)))
                 return rc;
     }
     if (sc.nc > 1 && cudaMemsetAsync(ws, 0xff, sc.sync(), st) != cudaSuccess) {
@@ -268,7 +268,7 @@ extern "C" {
 
 size_t lrscan_gates_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype, int dir) {
     if (call_shape(B, T, D, dtype) || B == 0 || T == 0 || D == 0 || dir < 0 || dir > 1) return 0;
-    return gates_scratch(B, T, D, dtype, dir).total();
+    return gates_scratch(B, T, D, dir).total();
 }
 
 int lrscan_fwd_gates(const lrscan_rows *r, const lrscan_rows *i, const lrscan_rows *x, const float *lam, float c,

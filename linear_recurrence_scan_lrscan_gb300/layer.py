@@ -14,7 +14,7 @@ import torch
 
 from . import lrscan as _l
 
-SAVE_EVERY = 64   # tokens between the states that the gated recurrence saves
+SAVE_EVERY = 16   # tokens between the states that the gated recurrence saves
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -117,7 +117,7 @@ def lrscan_fwd_gates(r, i, x, lam, *, c: float = 8.0, h0=None, segment_pos=None,
     restarting (a_t = 0) where the int32 [B, T] segment_pos is 0; r, i, x
     [B, T, D], lam fp32 [D].  Returns (out, last, saved): the states in the
     storage dtype, the fp32 [B, D] final state, and (want_saved) the fp32 states
-    before tokens 0, 64, 128, ... that the backward needs, else None."""
+    before tokens 0, 16, 32, ... that the backward needs, else None."""
     shape, code = _tokens(x)
     B, T, D = shape
     dev, dt = x.device, x.dtype

@@ -58,8 +58,8 @@ def check(s):
     R.assert_within(last, rlast, elast, torch.float32, "last")
     B, T, D = ref.shape
     h0 = torch.zeros((B, D), dtype=torch.float64) if s["h0"] is None else s["h0"].double().cpu()
-    before = torch.cat([h0[:, None], ref], 1)[:, :T:64]
-    ebefore = torch.cat([torch.zeros_like(h0)[:, None], e], 1)[:, :T:64]
+    before = torch.cat([h0[:, None], ref], 1)[:, :T:16]
+    ebefore = torch.cat([torch.zeros_like(h0)[:, None], e], 1)[:, :T:16]
     R.assert_within(saved, before, ebefore, torch.float32, "saved")
     grads = dict(zip(("grad_r", "grad_i", "grad_x", "grad_lam", "grad_h0"), run_bwd(s, saved)))
     want = R.backward(s["r"], s["i"], s["x"], s["lam"], s["go"], 8.0, s["h0"], s["seg"], s["gl"])
@@ -183,18 +183,15 @@ def test_gates_strided_gradients_and_layouts():
     run_bwd(s, run_fwd(s)[2], grad_r=both[..., :D], grad_i=both[..., D:])
     assert torch.equal(both[..., :D], ref[0]) and torch.equal(both[..., D:], ref[1])
     tm = {**s, **{k: s[k].transpose(0, 1).contiguous().transpose(0, 1) for k in ("r", "i", "x", "go")}}
-    out, last, saved = run_fwd(s)
-    o2, l2, s2 = run_fwd(tm, out=torch.empty((T, B, D), device="cuda", dtype=torch.bfloat16).transpose(0, 1))
-    assert torch.equal(out, o2) and torch.equal(last, l2)
-    assert all(torch.equal(a, b) for a, b in zip(ref, run_bwd(tm, s2)))
+    check(tm)  # plain loads instead of bulk copies: the same within the bounds, not bit for bit
+    time_major = torch.empty((T, B, D), device="cuda", dtype=torch.bfloat16).transpose(0, 1)
+    assert torch.equal(run_fwd(tm, out=time_major)[0], run_fwd(tm)[0])
     buf = torch.empty(B * T * D + 3, device="cuda", dtype=torch.bfloat16)
     shifted = buf[3:].view(B, T, D).copy_(s["x"])
-    o3, l3, _ = run_fwd({**s, "x": shifted})
-    assert torch.equal(out, o3) and torch.equal(last, l3)
+    check({**s, "x": shifted})
     # one gate for all requests: a broadcast input
     rb = s["r"][:1].expand(B, T, D)
-    o4 = run_fwd({**s, "r": rb})[0]
-    assert torch.equal(o4, run_fwd({**s, "r": rb.contiguous()})[0])
+    check({**s, "r": rb})
 
 
 def test_gates_autograd_and_differences():
