@@ -30,6 +30,7 @@ struct GatesArgs {
     RowsArg o0, o1, o2;           // forward: out; backward: grad_r, grad_i, grad_x
     const float *lam;             // [D]
     float c;
+    const float *rate;            // [D] c softplus(lam), or null: computed where it is used
     const float *h0;              // forward: [B, D] or null
     const float *grad_last;       // backward: [B, D] or null
     float *edge;                  // [B, D] or null: forward `last`, backward `grad_h0`
@@ -55,6 +56,9 @@ struct GatesLaunch {
 
 constexpr int kGatesTileRows = 64;  // tokens of a tile
 int gates_launch(const GatesLaunch &L, int dtype, int dir, int sm_count);
+// Sets the bytes (of a multiple of 16) at `words` to all ones and the rates.
+int gates_begin_launch(void *words, size_t bytes, const float *lam, float c, long long D, float *rate, int sm_count,
+                       cudaStream_t stream);
 // grad_lam from the partial sums part [rows][D], in a fixed order; `part` has
 // gates_finish_slices(rows) more rows after them.
 int gates_finish_slices(long long rows);

@@ -102,6 +102,15 @@ __device__ __forceinline__ void decay2(const float (&k)[2], const float (&rg)[2]
     mul_x2(s[0], s[1], y[0], y[1], rs[0], rs[1]);
 }
 
+// Before a launch whose tiles follow one another: nothing is published (all-ones
+// words), and every lane's rate is computed once.
+__global__ void __launch_bounds__(256) gates_begin_kernel(uint4 *words, long long n, const float *lam, float c, long long D,
+                                                          float *rate) {
+    const long long first = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, step = 256LL * gridDim.x;
+    for (long long j = first; j < n; j += step) words[j] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (long long d = first; d < D; d += step) rate[d] = gate_rate(__ldg(lam + d), c);
+}
+
 // ----------------------------------------------------------------------------
 // Maps h -> P h + Q.  A map with P = 0 (a segment starts inside) takes nothing
 // of what came before, not even an infinity.
@@ -123,6 +132,16 @@ template <bool SEG> __device__ __forceinline__ void join2(float (&P)[2], float (
     } else {
         fma_x2(Q[0], Q[1], m.x, m.y, Q[0], Q[1], m.z, m.w);
         mul_x2(P[0], P[1], m.x, m.y, P[0], P[1]);
+    }
+}
+
+// (P, Q) := (P, Q) o (P1, Q1)
+template <bool SEG>
+__device__ __forceinline__ void join2(float (&P)[2], float (&Q)[2], const float (&P1)[2], const float (&Q1)[2]) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        Q[v] = apply_map<SEG>(P[v], Q[v], Q1[v]);
+        P[v] = join_rate<SEG>(P[v], P1[v]);
     }
 }
 
@@ -204,19 +223,41 @@ __device__ __forceinline__ bool fold_list(const uint64_t *at, int n, float (&P)[
     return true;
 }
 
-// ----------------------------------------------------------------------------
-// Shared-memory plan, the same for both directions
-// ----------------------------------------------------------------------------
 struct GatesTile {
     int n, c, b, d0;  // n < 0: no more tiles
 };
 
+// Where the published words of lane 0 of tile c (in the order of the walk) of
+// lane tile n are: its own map; the maps of its group's 16 tiles; the state after
+// its 256.
+struct GatesWords {
+    uint64_t *tile, *group, *state;
+    int c, g1, g2;
+    bool closes;  // the last of its group, with tiles to come
+    __device__ GatesWords(const GatesArgs &g, const GatesTile &t) {
+        constexpr int R = kGatesRadix;
+        const int n1 = (g.nc + R - 1) / R, n2 = (n1 + R - 1) / R;
+        c = t.c;
+        g1 = c / R;
+        g2 = g1 / R;
+        tile = g.agg1 + (static_cast<size_t>(t.n) * g.nc + c) * kGatesLanes;
+        group = g.agg2 + (static_cast<size_t>(t.n) * n1 + g1) * kGatesLanes;
+        state = g.agg3 + (static_cast<size_t>(t.n) * n2 + g2) * kGatesLanes;
+        closes = c % R == R - 1 && c + 1 < g.nc;
+    }
+};
+
+// ----------------------------------------------------------------------------
+// Shared-memory plan, the same for both directions
+// ----------------------------------------------------------------------------
 constexpr int kTeamWarps = 4;
 constexpr int kTokens = 16;                        // a warp's
 constexpr int kTileRows = kTeamWarps * kTokens;
 static_assert(kTileRows == kGatesTileRows, "the host counts tiles alike");
 constexpr int kFolds = 3;
-constexpr int kSlots = 8;                          // of entering states: no tile is named this far ahead of its team
+constexpr int kSlots = 8;                          // of entering states
+constexpr int kRing = 16;                          // of tiles' names
+constexpr int kAhead = 1;                          // tiles named before a team is free for them
 
 // TEAMS teams, then the copy warp and the fold warps; S stages, TEAMS at least.
 template <class St, int TEAMS, int S, int PLANES, bool BULK> struct GatesGeo {
@@ -226,40 +267,38 @@ template <class St, int TEAMS, int S, int PLANES, bool BULK> struct GatesGeo {
     static constexpr int kThreads = (kWarps + 1 + kFolds) * 32;
     static constexpr int kPlane = kTileRows * kGatesLanes * static_cast<int>(sizeof(St));
     static constexpr int kStage = BULK ? PLANES * kPlane : 0;
-    static constexpr int kWords = kTileRows / 32;
     static constexpr int off_sum = S * kStage;                             // float4 [TEAMS][2][kTeamWarps][32]: a warp's map
     static constexpr int off_lam = off_sum + TEAMS * 2 * kTeamWarps * 32 * 16;  // float [TEAMS][2][kTeamWarps][64]
-    static constexpr int off_rate = off_lam + (PLANES == 4 ? TEAMS * 2 * kTeamWarps * 64 * 4 : 0);  // float [S][64]
-    static constexpr int off_in = off_rate + S * 64 * 4;                   // float [kSlots][64]
-    static constexpr int off_tile = off_in + kSlots * 64 * 4;              // GatesTile [S]
-    static constexpr int off_seg = off_tile + S * 16;                      // u32 [S][kWords]
-    static constexpr int off_bar = off_seg + S * kWords * 4;               // u64: GatesBars
-    static constexpr int off_flag = off_bar + (3 * S + 2 * kSlots) * 8;
+    static constexpr int off_in = off_lam + (PLANES == 4 ? TEAMS * 2 * kTeamWarps * 64 * 4 : 0);  // float [kSlots][64]
+    static constexpr int off_tile = off_in + kSlots * 64 * 4;              // GatesTile [kRing]
+    static constexpr int off_bar = off_tile + kRing * 16;               // u64: GatesBars
+    static constexpr int off_flag = off_bar + (2 * S + 2 * kSlots + kRing) * 8;
     static constexpr int kBytes = off_flag + 16 + 128;                     // and the base's alignment
+    static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
-// The barriers of the stages, and of the entering states.  Tile `it` of the CTA
-// has stage it % S, slot it % kSlots, team it % TEAMS and fold warp it % kFolds.
-// A wait on a phase's parity is exact only once the phase before it is over.
-// Tiles are named in order, so a warp that has had tile it - TEAMS (or it - 3)
-// may wait for tile it to be named: tile it - S was.  After that, the stage's
-// copies of tile it - S are over (its stage was emptied), so the wait on `full`
-// is exact too; and with S <= kSlots tile it is named only after the tiles
-// whose entering states used its slot two turns ago have left it.
+// The barriers.  Tile `it` of the CTA has stage it % S, slot it % kSlots, name
+// it % kRing, team it % TEAMS and fold warp it % kFolds.  A wait on a phase's
+// parity is exact only while that phase or the one before it is the barrier's
+// last.  Tiles are named in order, each once the team of tile it - S has
+// emptied the stage, and by then that team has left its tile before that, and so
+// have the fold warps: a name is kept for kRing tiles, an entering state for
+// kSlots.  A team waits for the name first: after it, the stage's earlier copies
+// are over and the wait on `full` is exact too.
 template <class Geo, int S> struct GatesBars {
     uint32_t named, full, empty, hfull, hempty;
     __device__ explicit GatesBars(char *smem) {
         named = smem_addr(smem) + Geo::off_bar;  // the tile is named
-        full = named + 8 * S;                    // and its planes, rates and restarts are in
-        empty = full + 8 * S;                    // the team and the fold warp are done with them
+        full = named + 8 * kRing;                // and its planes are in
+        empty = full + 8 * S;                    // the team is done with them
         hfull = empty + 8 * S;                   // the entering states are in
         hempty = hfull + 8 * kSlots;             // and have been read
     }
     __device__ void init() const {
+        for (int k = 0; k < kRing; ++k) mbar_init(named + 8 * k, 1);
         for (int s = 0; s < S; ++s) {
-            mbar_init(named + 8 * s, 1);
-            mbar_init(full + 8 * s, 2);
-            mbar_init(empty + 8 * s, kTeamWarps + 1);
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, kTeamWarps);
         }
         for (int k = 0; k < kSlots; ++k) {
             mbar_init(hfull + 8 * k, 1);
@@ -282,80 +321,52 @@ __device__ __forceinline__ bool tile_of(const GatesArgs &g, unsigned tk, GatesTi
     return there;
 }
 
-// The copy warp, both directions: takes tickets, names the stage's tile, copies
-// its planes in, and writes its lanes' rates and the tokens that start a
-// segment.  The next ticket is asked for, and a tile's rates and restarts are
-// read, while the stage is not yet free.
-template <class Geo, bool BULK, bool SEG, bool BWD, int PLANES, int S>
+// The copy warp, both directions (one thread of it): takes tickets, names the
+// tiles and copies their planes in.  The next ticket is asked for while the
+// stage is not yet free.
+template <class Geo, bool BULK, bool BWD, int PLANES, int S>
 __device__ __forceinline__ void gates_copy_warp(const GatesArgs &g, const CUtensorMap *const (&maps)[4], char *smem,
                                                 const GatesBars<Geo, S> &bars, const WaitCtx &wc) {
-    const int lane = threadIdx.x & 31;
-    float *rate = reinterpret_cast<float *>(smem + Geo::off_rate);
+    if ((threadIdx.x & 31) != 0) return;
     GatesTile *tile = reinterpret_cast<GatesTile *>(smem + Geo::off_tile);
-    uint32_t *segw = reinterpret_cast<uint32_t *>(smem + Geo::off_seg);
     const bool one = g.nc == 1;  // no tile waits for another: no tickets
-    auto ticket = [&](unsigned last) -> unsigned {  // lane 0's answer counts
-        if (one) return last + gridDim.x;
-        return lane == 0 ? atomicAdd(g.ticket, 1u) + 1u : 0u;  // the word starts as all ones
+    auto ticket = [&](unsigned last) -> unsigned {
+        return one ? last + gridDim.x : atomicAdd(g.ticket, 1u) + 1u;  // the word starts as all ones
     };
-    unsigned tk = one ? blockIdx.x : __shfl_sync(0xffffffffu, ticket(0), 0);
+    unsigned tk = one ? blockIdx.x : ticket(0);
     int issued = 0, ends = 0;
     bool ok = true;
     for (int it = 0;; ++it) {
         const int s = it % S;
         GatesTile t;
         const bool end = !tile_of(g, tk, t);
-        const long long t0 = static_cast<long long>(BWD ? g.nc - 1 - t.c : t.c) * kTileRows;
         unsigned next = tk;
-        float lam[2];
-        int seg[Geo::kWords];
-        if (!end) {
-            next = ticket(tk);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const int d = t.d0 + lane_at<BULK>(lane, v);
-                lam[v] = d < g.D ? __ldg(g.lam + d) : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < Geo::kWords; ++k) {
-                const long long row = t0 + 32 * k + lane;
-                seg[k] = SEG && row < g.T ? __ldg(g.seg + static_cast<long long>(t.b) * g.T + row) : 1;
-            }
-        }
+        if (!end) next = ticket(tk);
         ok = *wc.abort_flag == 0 && mbar_wait(bars.empty + 8 * s, ((it / S) & 1) ^ 1, wc, kSiteProducerEmpty);
-        ok = __all_sync(0xffffffffu, ok);
+        // a ticket taken long before a team is free holds up the tiles that
+        // follow it in other CTAs
+        const int before = it - Geo::kTeams - kAhead;
+        if (ok && before >= 0 && !end)
+            ok = mbar_wait(bars.hempty + 8 * (before % kSlots), (before / kSlots) & 1, wc, kSiteProducerEmpty);
         if (!ok) break;
-        if (lane == 0) {
-            tile[s] = t;
-            mbar_arrive(bars.named + 8 * s);
-            if (BULK && !end) {
-                mbar_arrive_expect_tx(bars.full + 8 * s, Geo::kStage);
-                const uint32_t dst = smem_addr(smem) + s * Geo::kStage;
+        tile[it % kRing] = t;
+        mbar_arrive(bars.named + 8 * (it % kRing));
+        if (BULK && !end) {
+            mbar_arrive_expect_tx(bars.full + 8 * s, Geo::kStage);
+            const uint32_t dst = smem_addr(smem) + s * Geo::kStage;
+            const int t0 = (BWD ? g.nc - 1 - t.c : t.c) * kTileRows;
 #pragma unroll
-                for (int p = 0; p < PLANES; ++p)
-                    tma_load_3d(dst + p * Geo::kPlane, maps[p], t.d0, static_cast<int>(t0), t.b, bars.full + 8 * s);
-            } else {
-                mbar_arrive(bars.full + 8 * s);
-            }
-        }
-        if (!end) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) rate[s * 64 + lane_at<BULK>(lane, v)] = gate_rate(lam[v], g.c);
-            if constexpr (SEG) {
-#pragma unroll
-                for (int k = 0; k < Geo::kWords; ++k) {
-                    const uint32_t bits = __ballot_sync(0xffffffffu, seg[k] == 0);
-                    if (lane == 0) segw[s * Geo::kWords + k] = bits;
-                }
-            }
+            for (int p = 0; p < PLANES; ++p)
+                tma_load_3d(dst + p * Geo::kPlane, maps[p], t.d0, t0, t.b, bars.full + 8 * s);
             issued = it + 1;
+        } else {
+            mbar_arrive(bars.full + 8 * s);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.full + 8 * s);
-        if (end && ++ends == (Geo::kTeams > kFolds ? Geo::kTeams : kFolds)) break;  // every team and fold warp has seen the end
-        tk = one ? next : __shfl_sync(0xffffffffu, next, 0);
+        // every team and fold warp sees an end of its own
+        if (end && ++ends == (Geo::kTeams > kFolds ? Geo::kTeams : kFolds)) break;
+        tk = next;
     }
-    if (BULK && !ok && lane == 0) {
+    if (BULK && !ok) {
         // leaving early: no copy of this CTA may still be on its way
         for (int it = issued > S ? issued - S : 0; it < issued; ++it) {
             const uint64_t start = global_timer_ns();
@@ -368,9 +379,26 @@ __device__ __forceinline__ void gates_copy_warp(const GatesArgs &g, const CUtens
     }
 }
 
+// The rates of this thread's two lanes, and the warp's tokens that start a
+// segment (bit l: token t0 + l).
+template <bool BULK>
+__device__ __forceinline__ void tile_rates(const GatesArgs &g, const GatesTile &t, int lane, bool (&in)[2], float (&k)[2]) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const int d = t.d0 + lane_at<BULK>(lane, v);
+        in[v] = d < g.D;
+        k[v] = 0.0f;
+        if (in[v]) k[v] = g.rate != nullptr ? __ldg(g.rate + d) : gate_rate(__ldg(g.lam + d), g.c);
+    }
+}
+__device__ __forceinline__ int first_token(const GatesArgs &g, const GatesTile &t, long long t0, int left, int lane) {
+    return lane < left ? __ldg(g.seg + t.b * g.T + t0 + lane) : 1;
+}
+
 // The fold warps, both directions: the state (or adjoint) that enters each of
-// the CTA's tiles, every kFolds-th tile to one warp, and the maps of groups of
-// tiles.  `start` [B, D]: what enters the first tile, or null for zeros.
+// the CTA's tiles, every kFolds-th tile to one warp, and the maps of the groups
+// that its tiles close.  `start` [B, D]: what enters
+// the first tile, or null for zeros.
 template <class Geo, bool BULK, bool SEG, int S>
 __device__ __forceinline__ void gates_fold_warp(const GatesArgs &g, const float *start, char *smem,
                                                 const GatesBars<Geo, S> &bars, int f, const WaitCtx &wc) {
@@ -378,59 +406,58 @@ __device__ __forceinline__ void gates_fold_warp(const GatesArgs &g, const float 
     const int lane = threadIdx.x & 31;  // tile lanes `lane` and 32 + lane: words are in the order of the lanes
     const GatesTile *tile = reinterpret_cast<const GatesTile *>(smem + Geo::off_tile);
     float *hin = reinterpret_cast<float *>(smem + Geo::off_in);
-    const int n1 = (g.nc + R - 1) / R, n2 = (n1 + R - 1) / R;
     for (int it = f;; it += kFolds) {
-        const int s = it % S, slot = it % kSlots;
-        if (!__all_sync(0xffffffffu, *wc.abort_flag == 0 && mbar_wait(bars.named + 8 * s, (it / S) & 1, wc, kSiteConsumerFull)))
+        const int slot = it % kSlots, name = it % kRing;
+        if (!__all_sync(0xffffffffu,
+                        *wc.abort_flag == 0 && mbar_wait(bars.named + 8 * name, (it / kRing) & 1, wc, kSiteConsumerFull)))
             return;
-        const GatesTile t = tile[s];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.empty + 8 * s);
+        const GatesTile t = tile[name];
         if (t.n < 0) return;
-        const int c = t.c, g1 = c / R, g2 = g1 / R;
-        const uint64_t *agg1 = g.agg1 + (static_cast<size_t>(t.n) * g.nc + g1 * R) * kGatesLanes + lane;  // its group
-        uint64_t *agg2 = g.agg2 + (static_cast<size_t>(t.n) * n1 + g2 * R) * kGatesLanes + lane;
-        uint64_t *agg3 = g.agg3 + (static_cast<size_t>(t.n) * n2 + g2) * kGatesLanes + lane;
-        const bool closes = c % R == R - 1 && c + 1 < g.nc;
+        const GatesWords at(g, t);
         float h[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
             const int d = t.d0 + lane + 32 * v;
-            if (start != nullptr && g2 == 0 && d < g.D) h[v] = __ldg(start + static_cast<long long>(t.b) * g.D + d);
+            if (start != nullptr && at.g2 == 0 && d < g.D) h[v] = __ldg(start + static_cast<long long>(t.b) * g.D + d);
         }
         // The tiles of the tile's own group before it; where it closes its
-        // group its own map next, so that the group's is out before anything
-        // of earlier groups is waited for; then what enters the group.
-        float P[2] = {1.0f, 1.0f}, Q[2] = {0.0f, 0.0f}, PC[2], QC[2];
+        // group its own map next, so that the group's is out before anything of
+        // earlier groups is waited for; the state that enters those; and the
+        // groups themselves.
+        float P[2] = {1.0f, 1.0f}, Q[2] = {0.0f, 0.0f}, PG[2] = {1.0f, 1.0f}, QG[2] = {0.0f, 0.0f};
         for (int step = 0; step < 4; ++step) {
-            const uint64_t *at = step == 0 ? agg1 : step == 1 ? agg1 + (c % R) * kGatesLanes : step == 2 ? agg3 - kGatesLanes : agg2;
-            const int n = step == 0 ? c % R : step == 1 ? (closes ? 1 : 0) : step == 2 ? (g2 > 0 ? 1 : 0) : g1 - g2 * R;
+            const int n = step == 0 ? at.c % R : step == 1 ? (at.closes ? 1 : 0) : step == 2 ? (at.g2 > 0 ? 1 : 0) : at.g1 % R;
             if (n == 0) continue;
-            float p[2] = {P[0], P[1]}, q[2] = {step < 2 ? Q[0] : h[0], step < 2 ? Q[1] : h[1]};
-            if (!fold_list<SEG>(at, n, p, q, wc)) return;
+            const uint64_t *end = step == 0 ? at.tile : step == 1 ? at.tile + kGatesLanes : step == 2 ? at.state : at.group;
+            float p[2] = {1.0f, 1.0f}, q[2] = {0.0f, 0.0f};
+            if (step == 1) {
+                p[0] = P[0]; p[1] = P[1];
+                q[0] = Q[0]; q[1] = Q[1];
+            }
+            if (!fold_list<SEG>(end - static_cast<size_t>(n) * kGatesLanes + lane, n, p, q, wc)) return;
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 if (step == 0) {
                     P[v] = p[v];
                     Q[v] = q[v];
                 } else if (step == 1) {
-                    PC[v] = p[v];
-                    QC[v] = q[v];
-                    publish1(agg2 + (g1 - g2 * R) * kGatesLanes + 32 * v, p[v], q[v]);
-                } else {
+                    publish1(at.group + lane + 32 * v, p[v], q[v]);
+                } else if (step == 2) {
                     h[v] = q[v];
+                } else {
+                    PG[v] = p[v];
+                    QG[v] = q[v];
                 }
             }
         }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) h[v] = apply_map<SEG>(PG[v], QG[v], h[v]);
         if (!__all_sync(0xffffffffu, mbar_wait(bars.hempty + 8 * slot, ((it / kSlots) & 1) ^ 1, wc, kSiteProducerEmpty)))
             return;
 #pragma unroll
         for (int v = 0; v < 2; ++v) hin[slot * 64 + lane + 32 * v] = apply_map<SEG>(P[v], Q[v], h[v]);
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.hfull + 8 * slot);
-        if (closes && c % (R * R) == R * R - 1)  // the state after these R * R tiles
-#pragma unroll
-            for (int v = 0; v < 2; ++v) publish1(agg3 + 32 * v, 0.0f, apply_map<SEG>(PC[v], QC[v], h[v]));
     }
 }
 
@@ -446,30 +473,41 @@ __device__ __forceinline__ float load_one(const St *p, bool in) {
     load_lanes_global<St, 1>(p, x);
     return x[0];
 }
-template <class St, bool BULK>
+// SLOW: lanes past the last are left out.
+template <class St, bool BULK, bool SLOW>
 __device__ __forceinline__ void store_pair(St *row, int lane, const bool (&in)[2], float y0, float y1) {
     if constexpr (BULK) {
         float y[2] = {y0, y1};
-        if (in[0]) store_lanes<St, 2>(row + 2 * lane, y);
+        if (!SLOW || in[0]) store_lanes<St, 2>(row + 2 * lane, y);
     } else {
         float u[1] = {y0}, w[1] = {y1};
-        if (in[0]) store_lanes<St, 1>(row + lane, u);
-        if (in[1]) store_lanes<St, 1>(row + lane + 32, w);
+        if (!SLOW || in[0]) store_lanes<St, 1>(row + lane, u);
+        if (!SLOW || in[1]) store_lanes<St, 1>(row + lane + 32, w);
     }
 }
 
-// A tile's map is out: two lanes of one warp.
+// The team's tile is out: (P, Q) its map, from the warp that has all of it.
 template <bool BULK>
 __device__ __forceinline__ void publish_tile(const GatesArgs &g, const GatesTile &t, int lane, const float (&P)[2],
                                              const float (&Q)[2]) {
-    uint64_t *at = g.agg1 + (static_cast<size_t>(t.n) * g.nc + t.c) * kGatesLanes;
+    const GatesWords at(g, t);
 #pragma unroll
-    for (int v = 0; v < 2; ++v) publish1(at + lane_at<BULK>(lane, v), P[v], Q[v]);
+    for (int v = 0; v < 2; ++v) publish1(at.tile + lane_at<BULK>(lane, v), P[v], Q[v]);
+}
+// After the last tile of 256: the state it leaves.
+template <bool BULK, bool SEG>
+__device__ __forceinline__ void publish_state(const GatesArgs &g, const GatesTile &t, int lane, const float (&P)[2],
+                                              const float (&Q)[2], const float (&h)[2]) {
+    constexpr int R = kGatesRadix;
+    const GatesWords at(g, t);
+    if (!at.closes || t.c % (R * R) != R * R - 1) return;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) publish1(at.state + lane_at<BULK>(lane, v), 0.0f, apply_map<SEG>(P[v], Q[v], h[v]));
 }
 
 // Two lanes of token `row` of plane p: from the stage, or from memory (t0 + l
 // the token, l < left).
-template <class St, class Geo, bool BULK>
+template <class St, class Geo, bool BULK, bool SLOW>
 __device__ __forceinline__ void plane_pair(const char *stage, int p, int row, const RowsArg &m, long long at, int l,
                                            const bool (&in)[2], int left, int lane, float (&x)[2]) {
     if constexpr (BULK) {
@@ -477,7 +515,7 @@ __device__ __forceinline__ void plane_pair(const char *stage, int p, int row, co
     } else {
 #pragma unroll
         for (int v = 0; v < 2; ++v)
-            x[v] = load_one(static_cast<const St *>(m.p) + at + l * m.st + lane_at<BULK>(lane, v), in[v] && l < left);
+            x[v] = load_one(static_cast<const St *>(m.p) + at + l * m.st + lane_at<BULK>(lane, v), !SLOW || (in[v] && l < left));
     }
 }
 
@@ -495,9 +533,9 @@ __device__ __forceinline__ void gates_fwd_tokens(const GatesArgs &g, const char 
 #pragma unroll
     for (int l = 0; l < L; ++l) {
         float r[2], i[2], x[2], rg[2], ig[2], G[2], sq[2], rs[2];
-        plane_pair<St, Geo, BULK>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
-        plane_pair<St, Geo, BULK>(stage, 1, row0 + l, g.i, ai, l, in, left, lane, i);
-        plane_pair<St, Geo, BULK>(stage, 2, row0 + l, g.x, ax, l, in, left, lane, x);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 1, row0 + l, g.i, ai, l, in, left, lane, i);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 2, row0 + l, g.x, ax, l, in, left, lane, x);
         sigmoid2(rg, r);
         sigmoid2(ig, i);
         decay2<SLOW>(k, rg, G, a[l], sq, rs);
@@ -525,6 +563,25 @@ __device__ __forceinline__ void gates_fwd_tokens(const GatesArgs &g, const char 
     }
 }
 
+// The states of the warp's tokens from h on, stored.
+template <class St, bool BULK, bool SEG, bool SLOW>
+__device__ __forceinline__ void gates_fwd_states(const GatesArgs &g, const GatesTile &t, long long t0, const bool (&in)[2],
+                                                 int left, int lane, uint32_t first, const float (&a)[kTokens][2],
+                                                 const float (&b)[kTokens][2], float (&h)[2]) {
+    St *out = static_cast<St *>(g.o0.p) + t.b * g.o0.sb + t0 * g.o0.st + t.d0;
+#pragma unroll
+    for (int l = 0; l < kTokens; ++l) {
+        if (SEG && ((first >> l) & 1u)) {
+            h[0] = b[l][0];
+            h[1] = b[l][1];
+        } else {
+            fma_x2(h[0], h[1], a[l][0], a[l][1], h[0], h[1], b[l][0], b[l][1]);
+        }
+        if (!SLOW || l < left) store_pair<St, BULK, SLOW>(out, lane, in, h[0], h[1]);
+        out += g.o0.st;
+    }
+}
+
 template <class St, int TEAMS, int S, bool BULK, bool SEG>
 __global__ void __launch_bounds__(GatesGeo<St, TEAMS, S, 3, BULK>::kThreads, 1)
 gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mi,
@@ -544,7 +601,7 @@ gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
     __syncthreads();
     if (threadIdx.x / 32 == Geo::kWarps) {
         const CUtensorMap *const maps[4] = {&mr, &mi, &mx, nullptr};
-        gates_copy_warp<Geo, BULK, SEG, false, 3, S>(g, maps, smem, bars, wc);
+        gates_copy_warp<Geo, BULK, false, 3, S>(g, maps, smem, bars, wc);
         return;
     }
     if (threadIdx.x / 32 > Geo::kWarps) {
@@ -553,34 +610,34 @@ gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
     }
     const int team = threadIdx.x / (32 * kTeamWarps), warp = threadIdx.x / 32 % kTeamWarps;
     const GatesTile *tile = reinterpret_cast<const GatesTile *>(smem + Geo::off_tile);
-    const float *rate = reinterpret_cast<const float *>(smem + Geo::off_rate);
     const float *hin = reinterpret_cast<const float *>(smem + Geo::off_in);
-    const uint32_t *segw = reinterpret_cast<const uint32_t *>(smem + Geo::off_seg);
     float4 *sums = reinterpret_cast<float4 *>(smem + Geo::off_sum) + team * 2 * kTeamWarps * 32;
     const long long ns = (g.T + kGatesSave - 1) / kGatesSave;
     bool ok = true;
     for (int it = team, turn = 0;; it += TEAMS, turn ^= 1) {
         const int s = it % S, slot = it % kSlots;
-        ok = ok && *flag == 0 && mbar_wait(bars.named + 8 * s, (it / S) & 1, wc, kSiteConsumerFull) &&
-             mbar_wait(bars.full + 8 * s, (it / S) & 1, wc, kSiteConsumerFull);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && *flag == 0 && mbar_wait(bars.named + 8 * (it % kRing), (it / kRing) & 1, wc, kSiteConsumerFull);
         GatesTile t{-1, 0, 0, 0};
-        if (ok) t = tile[s];
+        if (ok) t = tile[it % kRing];
         const long long t0 = static_cast<long long>(t.c) * kTileRows + warp * L;  // this warp's first token
-        const int left = g.T - t0 < L ? static_cast<int>(g.T > t0 ? g.T - t0 : 0) : L;
-        bool in[2];
+        const int left = t.n < 0 || g.T <= t0 ? 0 : g.T - t0 < L ? static_cast<int>(g.T - t0) : L;
+        bool in[2] = {false, false};
+        float k[2] = {0.0f, 0.0f};
+        int seg = 1;
+        if (t.n >= 0) {  // on their way while the planes come in
+            tile_rates<BULK>(g, t, lane, in, k);
+            if constexpr (SEG) seg = first_token(g, t, t0, left, lane);
+        }
+        ok = ok && mbar_wait(bars.full + 8 * s, (it / S) & 1, wc, kSiteConsumerFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) t.n = -1;
         float a[L][2], b[L][2], P[2], Q[2];
         uint32_t first = 0;
+        bool slow = false;
         float4 *sum = sums + turn * kTeamWarps * 32;
         if (t.n >= 0) {
-            float k[2];
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                in[v] = t.d0 + lane_at<BULK>(lane, v) < g.D;
-                k[v] = rate[s * 64 + lane_at<BULK>(lane, v)];
-            }
-            if constexpr (SEG) first = segw[s * Geo::kWords + warp / 2] >> (16 * (warp & 1));
-            const bool slow = left < L || !__all_sync(0xffffffffu, k[0] <= 0.25f && k[1] <= 0.25f);
+            if constexpr (SEG) first = __ballot_sync(0xffffffffu, seg == 0);
+            slow = left < L || !__all_sync(0xffffffffu, in[0] && in[1] && k[0] <= 0.25f && k[1] <= 0.25f);
             const char *stage = smem + s * Geo::kStage;
             const long long ar = t.b * g.r.sb + t0 * g.r.st + t.d0, ai = t.b * g.i.sb + t0 * g.i.st + t.d0,
                             ax = t.b * g.x.sb + t0 * g.x.st + t.d0;
@@ -600,15 +657,16 @@ gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
 #pragma unroll
         for (int w = 0; w < kTeamWarps - 1; ++w)
             if (w < warp) join2<SEG>(Pe, Qe, sum[w * 32 + lane]);
-        if (warp == kTeamWarps - 1 && t.c + 1 < g.nc) {
-            float Pt[2] = {Pe[0], Pe[1]}, Qt[2] = {Qe[0], Qe[1]};
-            join2<SEG>(Pt, Qt, make_float4(P[0], P[1], Q[0], Q[1]));
-            publish_tile<BULK>(g, t, lane, Pt, Qt);
-        }
+        join2<SEG>(P, Q, Pe, Qe);  // from the tile's start to this warp's end
+        if (warp == kTeamWarps - 1 && t.c + 1 < g.nc) publish_tile<BULK>(g, t, lane, P, Q);
         ok = __all_sync(0xffffffffu, mbar_wait(bars.hfull + 8 * slot, (it / kSlots) & 1, wc, kSiteGatesRow));
         float h[2];
 #pragma unroll
         for (int v = 0; v < 2; ++v) h[v] = apply_map<SEG>(Pe[v], Qe[v], hin[slot * 64 + lane_at<BULK>(lane, v)]);
+        if (warp == kTeamWarps - 1 && ok) {
+            const float he[2] = {hin[slot * 64 + lane_at<BULK>(lane, 0)], hin[slot * 64 + lane_at<BULK>(lane, 1)]};
+            publish_state<BULK, SEG>(g, t, lane, P, Q, he);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.hempty + 8 * slot);
         if (!ok) continue;  // the next barrier stops the team
@@ -618,18 +676,10 @@ gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
             for (int v = 0; v < 2; ++v)
                 if (in[v]) to[lane_at<BULK>(lane, v)] = h[v];
         }
-        St *out = static_cast<St *>(g.o0.p) + t.b * g.o0.sb + t0 * g.o0.st + t.d0;
-#pragma unroll
-        for (int l = 0; l < L; ++l) {
-            if (SEG && ((first >> l) & 1u)) {
-                h[0] = b[l][0];
-                h[1] = b[l][1];
-            } else {
-                fma_x2(h[0], h[1], a[l][0], a[l][1], h[0], h[1], b[l][0], b[l][1]);
-            }
-            if (l < left) store_pair<St, BULK>(out, lane, in, h[0], h[1]);
-            out += g.o0.st;
-        }
+        if (slow)
+            gates_fwd_states<St, BULK, SEG, true>(g, t, t0, in, left, lane, first, a, b, h);
+        else
+            gates_fwd_states<St, BULK, SEG, false>(g, t, t0, in, left, lane, first, a, b, h);
         if (warp == kTeamWarps - 1 && t.c + 1 == g.nc && g.edge != nullptr) {
 #pragma unroll
             for (int v = 0; v < 2; ++v)
@@ -662,8 +712,8 @@ __device__ __forceinline__ void gates_bwd_decays(const GatesArgs &g, const char 
 #pragma unroll
     for (int l = kTokens - 1; l >= 0; --l) {
         float r[2], go[2], rg[2], G[2], m[2];
-        plane_pair<St, Geo, BULK>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
-        plane_pair<St, Geo, BULK>(stage, 3, row0 + l, g.go, ag, l, in, left, lane, go);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 3, row0 + l, g.go, ag, l, in, left, lane, go);
         sigmoid2(rg, r);
         decay_only2<SLOW>(k, rg, G, a[l], m);
         if (SLOW && l >= left) a[l][0] = a[l][1] = 1.0f;
@@ -676,6 +726,26 @@ __device__ __forceinline__ void gates_bwd_decays(const GatesArgs &g, const char 
             mul_x2(Q[0], Q[1], Q[0], Q[1], a[l][0], a[l][1]);
             mul_x2(P[0], P[1], P[0], P[1], a[l][0], a[l][1]);
         }
+    }
+}
+
+// Second walk, last token to first, from the adjoint cc that enters: the decays
+// become the adjoints.
+template <class St, class Geo, bool BULK, bool SEG, bool SLOW>
+__device__ __forceinline__ void gates_bwd_adjoints(const GatesArgs &g, const char *stage, int row0, long long ag,
+                                                   const bool (&in)[2], int left, int lane, uint32_t first,
+                                                   float (&a)[kTokens][2], float (&cc)[2]) {
+#pragma unroll
+    for (int l = kTokens - 1; l >= 0; --l) {
+        float go[2];
+        plane_pair<St, Geo, BULK, SLOW>(stage, 3, row0 + l, g.go, ag, l, in, left, lane, go);
+        add_x2(go[0], go[1], go[0], go[1], cc[0], cc[1]);
+        if (SEG && ((first >> l) & 1u))
+            cc[0] = cc[1] = 0.0f;
+        else
+            mul_x2(cc[0], cc[1], go[0], go[1], a[l][0], a[l][1]);
+        a[l][0] = go[0];
+        a[l][1] = go[1];
     }
 }
 
@@ -695,9 +765,9 @@ __device__ __forceinline__ void gates_bwd_grads(const GatesArgs &g, const char *
     for (int l = 0; l < kTokens; ++l) {
         if (SLOW && l >= left) break;
         float r[2], i[2], x[2], rg[2], ig[2], G[2], a[2], sq[2], rs[2], ix[2], q[2], yr[2], yi[2], yx[2], w[2], z[2];
-        plane_pair<St, Geo, BULK>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
-        plane_pair<St, Geo, BULK>(stage, 1, row0 + l, g.i, ai, l, in, left, lane, i);
-        plane_pair<St, Geo, BULK>(stage, 2, row0 + l, g.x, ax, l, in, left, lane, x);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 1, row0 + l, g.i, ai, l, in, left, lane, i);
+        plane_pair<St, Geo, BULK, SLOW>(stage, 2, row0 + l, g.x, ax, l, in, left, lane, x);
         sigmoid2(rg, r);
         sigmoid2(ig, i);
         decay2<SLOW>(k, rg, G, a, sq, rs);
@@ -727,9 +797,9 @@ __device__ __forceinline__ void gates_bwd_grads(const GatesArgs &g, const char *
             mul_x2(ix[0], ix[1], ix[0], ix[1], sq[0], sq[1]);
             fma_x2(h[0], h[1], a[0], a[1], h[0], h[1], ix[0], ix[1]);
         }
-        store_pair<St, BULK>(gr, lane, in, yr[0], yr[1]);
-        store_pair<St, BULK>(gi, lane, in, yi[0], yi[1]);
-        store_pair<St, BULK>(gx, lane, in, yx[0], yx[1]);
+        store_pair<St, BULK, SLOW>(gr, lane, in, yr[0], yr[1]);
+        store_pair<St, BULK, SLOW>(gi, lane, in, yi[0], yi[1]);
+        store_pair<St, BULK, SLOW>(gx, lane, in, yx[0], yx[1]);
         gr += g.o0.st;
         gi += g.o1.st;
         gx += g.o2.st;
@@ -756,7 +826,7 @@ gates_bwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
     __syncthreads();
     if (threadIdx.x / 32 == Geo::kWarps) {
         const CUtensorMap *const maps[4] = {&mr, &mi, &mx, &mg};
-        gates_copy_warp<Geo, BULK, SEG, true, 4, S>(g, maps, smem, bars, wc);
+        gates_copy_warp<Geo, BULK, true, 4, S>(g, maps, smem, bars, wc);
         return;
     }
     if (threadIdx.x / 32 > Geo::kWarps) {
@@ -765,9 +835,7 @@ gates_bwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
     }
     const int team = threadIdx.x / (32 * kTeamWarps), warp = threadIdx.x / 32 % kTeamWarps;
     const GatesTile *tile = reinterpret_cast<const GatesTile *>(smem + Geo::off_tile);
-    const float *rate = reinterpret_cast<const float *>(smem + Geo::off_rate);
     const float *cin = reinterpret_cast<const float *>(smem + Geo::off_in);
-    const uint32_t *segw = reinterpret_cast<const uint32_t *>(smem + Geo::off_seg);
     float4 *sums = reinterpret_cast<float4 *>(smem + Geo::off_sum) + team * 2 * kTeamWarps * 32;
     float *lams = reinterpret_cast<float *>(smem + Geo::off_lam) + team * 2 * kTeamWarps * 64;
     const long long ns = (g.T + kGatesSave - 1) / kGatesSave;
@@ -776,31 +844,35 @@ gates_bwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
     bool ok = true;
     for (int it = team, turn = 0;; it += TEAMS, turn ^= 1) {
         const int s = it % S, slot = it % kSlots;
-        ok = ok && *flag == 0 && mbar_wait(bars.named + 8 * s, (it / S) & 1, wc, kSiteConsumerFull) &&
-             mbar_wait(bars.full + 8 * s, (it / S) & 1, wc, kSiteConsumerFull);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && *flag == 0 && mbar_wait(bars.named + 8 * (it % kRing), (it / kRing) & 1, wc, kSiteConsumerFull);
         GatesTile t{-1, 0, 0, 0};
-        if (ok) t = tile[s];
+        if (ok) t = tile[it % kRing];
         const int ct = g.nc - 1 - t.c;  // the tile's place in time
         const long long t0 = static_cast<long long>(ct) * kTileRows + warp * L;
-        const int left = g.T - t0 < L ? static_cast<int>(g.T > t0 ? g.T - t0 : 0) : L;
+        const int left = t.n < 0 || g.T <= t0 ? 0 : g.T - t0 < L ? static_cast<int>(g.T - t0) : L;
         bool in[2] = {false, false};
-        float a[L][2], k[2], h[2] = {0.0f, 0.0f}, P[2], Q[2];
+        float k[2] = {0.0f, 0.0f}, h[2] = {0.0f, 0.0f};
+        int seg = 1;
+        if (t.n >= 0) {  // on their way while the planes come in
+            tile_rates<BULK>(g, t, lane, in, k);
+            if constexpr (SEG) seg = first_token(g, t, t0, left, lane);
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                if (in[v] && left > 0)
+                    h[v] = __ldg(g.saved + (t.b * ns + t0 / kGatesSave) * g.D + t.d0 + lane_at<BULK>(lane, v));
+        }
+        ok = ok && mbar_wait(bars.full + 8 * s, (it / S) & 1, wc, kSiteConsumerFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) t.n = -1;
+        float a[L][2], P[2], Q[2];
         uint32_t first = 0;
         bool slow = false;
         const char *stage = smem + s * Geo::kStage;
         const long long ag = t.b * g.go.sb + t0 * g.go.st + t.d0;
         float4 *sum = sums + turn * kTeamWarps * 32;
         if (t.n >= 0) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const int d = t.d0 + lane_at<BULK>(lane, v);
-                in[v] = d < g.D;
-                k[v] = rate[s * 64 + lane_at<BULK>(lane, v)];
-                if (in[v] && left > 0) h[v] = __ldg(g.saved + (t.b * ns + t0 / kGatesSave) * g.D + d);
-            }
-            if constexpr (SEG) first = segw[s * Geo::kWords + warp / 2] >> (16 * (warp & 1));
-            slow = left < L || !__all_sync(0xffffffffu, k[0] <= 0.25f && k[1] <= 0.25f);
+            if constexpr (SEG) first = __ballot_sync(0xffffffffu, seg == 0);
+            slow = left < L || !__all_sync(0xffffffffu, in[0] && in[1] && k[0] <= 0.25f && k[1] <= 0.25f);
             const long long ar = t.b * g.r.sb + t0 * g.r.st + t.d0;
             if (slow)
                 gates_bwd_decays<St, Geo, BULK, SEG, true>(g, stage, warp * L, ar, ag, in, left, lane, k, first, a, P, Q);
@@ -828,32 +900,23 @@ gates_bwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
 #pragma unroll
         for (int w = kTeamWarps - 1; w > 0; --w)
             if (w > warp) join2<SEG>(Pe, Qe, sum[w * 32 + lane]);
-        if (warp == 0 && t.c + 1 < g.nc) {
-            float Pt[2] = {Pe[0], Pe[1]}, Qt[2] = {Qe[0], Qe[1]};
-            join2<SEG>(Pt, Qt, make_float4(P[0], P[1], Q[0], Q[1]));
-            publish_tile<BULK>(g, t, lane, Pt, Qt);
-        }
+        join2<SEG>(P, Q, Pe, Qe);  // from the tile's end to this warp's start
+        if (warp == 0 && t.c + 1 < g.nc) publish_tile<BULK>(g, t, lane, P, Q);
         ok = __all_sync(0xffffffffu, mbar_wait(bars.hfull + 8 * slot, (it / kSlots) & 1, wc, kSiteGatesRow));
         float cc[2];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) cc[v] = apply_map<SEG>(Pe[v], Qe[v], cin[slot * 64 + lane_at<BULK>(lane, v)]);
+        for (int v = 0; v < 2; ++v) cc[v] = cin[slot * 64 + lane_at<BULK>(lane, v)];
+        if (warp == 0 && ok) publish_state<BULK, SEG>(g, t, lane, P, Q, cc);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) cc[v] = apply_map<SEG>(Pe[v], Qe[v], cc[v]);
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.hempty + 8 * slot);
         float ql[2] = {0.0f, 0.0f};
         if (ok) {
-            // second walk, last token to first: the decays become the adjoints
-#pragma unroll
-            for (int l = L - 1; l >= 0; --l) {
-                float go[2];
-                plane_pair<St, Geo, BULK>(stage, 3, warp * L + l, g.go, ag, l, in, left, lane, go);
-                add_x2(go[0], go[1], go[0], go[1], cc[0], cc[1]);
-                if (SEG && ((first >> l) & 1u))
-                    cc[0] = cc[1] = 0.0f;
-                else
-                    mul_x2(cc[0], cc[1], go[0], go[1], a[l][0], a[l][1]);
-                a[l][0] = go[0];
-                a[l][1] = go[1];
-            }
+            if (slow)
+                gates_bwd_adjoints<St, Geo, BULK, SEG, true>(g, stage, warp * L, ag, in, left, lane, first, a, cc);
+            else
+                gates_bwd_adjoints<St, Geo, BULK, SEG, false>(g, stage, warp * L, ag, in, left, lane, first, a, cc);
             if (slow)
                 gates_bwd_grads<St, Geo, BULK, SEG, true>(g, stage, warp * L, t, t0, in, left, lane, k, first, a, h, ql);
             else

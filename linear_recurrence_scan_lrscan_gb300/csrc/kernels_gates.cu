@@ -14,7 +14,7 @@ constexpr int kMaxDev = 64;
 template <class St, int DIR> struct Shape;
 template <> struct Shape<float, 0> { static constexpr int teams = 4, stages = 4; };
 template <> struct Shape<float, 1> { static constexpr int teams = 3, stages = 3; };
-template <> struct Shape<bf16_t, 0> { static constexpr int teams = 4, stages = 8; };
+template <> struct Shape<bf16_t, 0> { static constexpr int teams = 4, stages = 6; };
 template <> struct Shape<bf16_t, 1> { static constexpr int teams = 4, stages = 6; };
 
 // CTAs of `kern` that fit on an SM (asked once per device), its shared memory allowed.
@@ -117,6 +117,15 @@ template <class St> __global__ void __launch_bounds__(256) gates_step_kernel(con
 
 int gates_launch(const GatesLaunch &L, int dtype, int dir, int sm_count) {
     return dtype == 0 ? pick<float>(L, dir, sm_count) : pick<bf16_t>(L, dir, sm_count);
+}
+
+int gates_begin_launch(void *words, size_t bytes, const float *lam, float c, long long D, float *rate, int sm_count,
+                       cudaStream_t stream) {
+    const long long n = static_cast<long long>(bytes / 16), most = n > D ? n : D;
+    const long long blocks = (most + 255) / 256;
+    gates_begin_kernel<<<static_cast<unsigned>(blocks < 4LL * sm_count ? blocks : 4LL * sm_count), 256, 0, stream>>>(
+        static_cast<uint4 *>(words), n, lam, c, D, rate);
+    return cudaGetLastError() != cudaSuccess;
 }
 
 int gates_finish_slices(long long rows) { return column_slices(rows); }

@@ -66,12 +66,12 @@ int launch_failed(const char *what) {
 // ----------------------------------------------------------------------------
 struct GatesScratch {
     int64_t nl, nc, n1, n2;
-    size_t head, a1, a2, a3, part;  // bytes
+    size_t head, a1, a2, a3, rate, part;  // bytes
     size_t sync() const { return head + a1 + a2 + a3; }
-    size_t total() const { return sync() + part; }
+    size_t total() const { return sync() + rate + part; }
 };
-// Ticket and published maps (only where tiles follow one another in time),
-// then the backward's partial sums of the lam gradient.
+// Ticket, published maps and rates (only where tiles follow one another in
+// time), then the backward's partial sums of the lam gradient.
 GatesScratch gates_scratch(int64_t B, int64_t T, int64_t D, int dir) {
     GatesScratch s{};
     const int64_t rows = kGatesTileRows;
@@ -85,6 +85,7 @@ GatesScratch gates_scratch(int64_t B, int64_t T, int64_t D, int dir) {
         s.a1 = pad256(tile * s.nc);
         s.a2 = pad256(tile * s.n1);
         s.a3 = pad256(tile * s.n2);
+        s.rate = pad256(static_cast<size_t>(D) * 4);
     }
     if (dir == 1) s.part = pad256(static_cast<size_t>(B * s.nc + gates_finish_slices(B * s.nc)) * D * 4);
     return s;
@@ -137,8 +138,9 @@ int gates_run(GatesLaunch *L, int dtype, int dir, float *grad_lam, void *stream,
         a.agg1 = reinterpret_cast<uint64_t *>(base + sc.head);
         a.agg2 = reinterpret_cast<uint64_t *>(base + sc.head + sc.a1);
         a.agg3 = reinterpret_cast<uint64_t *>(base + sc.head + sc.a1 + sc.a2);
+        a.rate = reinterpret_cast<float *>(base + sc.sync());
     }
-    if (dir == 1) a.part = reinterpret_cast<float *>(base + sc.sync());
+    if (dir == 1) a.part = reinterpret_cast<float *>(base + sc.sync() + sc.rate);
     a.status = ctx.status;
     a.timeout_ns = ctx.timeout_ns;
     L->stream = st;
@@ -149,10 +151,8 @@ int gates_run(GatesLaunch *L, int dtype, int dir, float *grad_lam, void *stream,
                                       kGatesTileRows)))
                 return rc;
     }
-    if (sc.nc > 1 && cudaMemsetAsync(ws, 0xff, sc.sync(), st) != cudaSuccess) {
-        cudaGetLastError();
-        return report_errorf(LRSCAN_ECUDA, "clearing the workspace failed");
-    }
+    if (sc.nc > 1 && gates_begin_launch(ws, sc.sync(), a.lam, a.c, D, const_cast<float *>(a.rate), ctx.sm_count, st))
+        return launch_failed("the gated recurrence's first kernel");
     if (gates_launch(*L, dtype, dir, ctx.sm_count)) return launch_failed("the gated recurrence");
     if (dir == 1 && gates_finish_launch(a.part, B * sc.nc, D, a.lam, grad_lam, st))
         return launch_failed("the reduction of grad_lam");
