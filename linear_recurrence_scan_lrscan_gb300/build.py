@@ -17,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "liblrscan.so")
+BINDING = os.path.join(BUILD, "lrscan_layer.so")  # Python binding of the operators around the scan
 SOURCES = ["lrscan_abi.cu", "kernels_window.cu", "kernels_window_state.cu", "kernels_chunk.cu", "kernels_complex.cu", "kernels_complex_state.cu", "kernels_complex_chunk.cu", "kernels_stream.cu", "kernels_gated.cu", "kernels_gates.cu", "kernels_conv.cu", "kernels_embed.cu", "layer_abi.cu", "noalloc_chunk.cu", "host_pipeline.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -35,6 +36,20 @@ def cuda_lib_dir(nvcc: str) -> str:
 def compile_flags(extra=()) -> list[str]:
     return [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
             "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}", *extra]
+
+
+def binding_command(out: str) -> list[str]:
+    """The host compiler's command for layer_binding.cpp, against this Python and this torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(cuda_lib_dir(_nvcc()))
+    includes = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(), os.path.join(cuda, "include"), INCLUDE]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[x for i in includes for x in ("-isystem", i)], os.path.join(CSRC, "layer_binding.cpp"), "-o", out,
+            f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _stale(out: str, deps: list[str]) -> bool:
@@ -57,18 +72,25 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         if force or _stale(obj, [path, *headers]):
             jobs.append([nvcc, *compile_flags(extra_flags), "-c", path, "-o", obj])
 
+    binding = BINDING + f".tmp{os.getpid()}"
+    bind = force or _stale(BINDING, [os.path.join(CSRC, "layer_binding.cpp"), os.path.join(INCLUDE, "lrscan.h")])
+    if bind:
+        jobs.append(binding_command(binding))
+
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compiling failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, file=sys.stderr)
         return r
 
     with cf.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
         list(ex.map(run, jobs))
+    if bind:
+        os.replace(binding, BINDING)
     if force or jobs or _stale(LIB, objs):
         libdir = cuda_lib_dir(nvcc)
         tmp = LIB + f".tmp{os.getpid()}"
