@@ -7,6 +7,9 @@
 
 #include <cuda_runtime.h>
 
+#include "launch.h"
+#include "scan_common.cuh"
+
 namespace lrscan {
 
 template <class Put>
@@ -17,6 +20,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float *part, lo
     const long long per = (rows + gridDim.y - 1) / gridDim.y;
     const long long r0 = per * blockIdx.y, r1 = r0 + per < rows ? r0 + per : rows;
     float sum = 0.0f;
+    pdl_wait();
     if (d < cols) {
 #pragma unroll 8
         for (long long r = r0 + warp; r < r1; r += 32) sum += __ldg(part + r * cols + d);
@@ -46,14 +50,16 @@ inline int column_slices(long long rows) {
 template <class Put> int column_sums(float *part, long long rows, long long cols, const Put &put, cudaStream_t st) {
     const int slices = column_slices(rows);
     const unsigned x = static_cast<unsigned>((cols + 31) / 32);
-    if (slices == 1) {
-        column_sums_kernel<Put><<<dim3(x, 1), 1024, 0, st>>>(part, rows, cols, put);
-    } else {
+    cudaError_t e = cudaSuccess;
+    if (slices > 1) {
         float *second = part + rows * cols;
-        column_sums_kernel<PutSlice><<<dim3(x, slices), 1024, 0, st>>>(part, rows, cols, PutSlice{second, cols});
-        column_sums_kernel<Put><<<dim3(x, 1), 1024, 0, st>>>(second, slices, cols, put);
+        e = launch_pdl(column_sums_kernel<PutSlice>, dim3(x, slices), dim3(1024), 0, st, part, rows, cols,
+                       PutSlice{second, cols});
+        part = second;
+        rows = slices;
     }
-    return cudaGetLastError() != cudaSuccess;
+    if (e == cudaSuccess) e = launch_pdl(column_sums_kernel<Put>, dim3(x, 1), dim3(1024), 0, st, part, rows, cols, put);
+    return e != cudaSuccess;
 }
 
 }  // namespace lrscan

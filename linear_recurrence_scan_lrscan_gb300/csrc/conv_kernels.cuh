@@ -10,17 +10,45 @@
 // A thread walks kConvSteps tokens of V lanes with the last K - 1 tokens in
 // registers, so that HBM carries each element once (the tokens that two walks
 // share come from L2); a warp covers 32 V neighbouring lanes, a CTA
-// kConvSplit walks one after another in time.  `run` counts the tokens before
-// t that are in t's segment.
+// kConvSplit walks one after another in time.  The tokens that start a segment
+// are one word of bits a walk, the same for the whole warp: eight tokens that no
+// restart touches take a path without conditions, two lanes an instruction.
 #pragma once
 
 #include "conv_args.h"
+#include "packed_f32x2.cuh"
 #include "scan_common.cuh"
 
 namespace lrscan {
 
-// Tokens read ahead by a walk.
-constexpr int kConvAhead = 8;
+// Bytes of each plane that a thread has in flight, and the tokens they are.
+template <class St, int V, int PLANES> struct ConvAhead {
+    static constexpr int bytes = PLANES == 1 ? 128 : 64;
+    static constexpr int per = V * static_cast<int>(sizeof(St));
+    static constexpr int tokens = bytes / per < 8 ? bytes / per : bytes / per > 16 ? 16 : bytes / per;
+};
+
+// The tokens t0 - (K-1) .. t0 + kConvSteps + K - 2 that start a segment, bit 0
+// the first of them; the whole warp calls it.
+template <int K> __device__ __forceinline__ uint64_t conv_starts(const int32_t *seg, long long t0, long long T) {
+    if (seg == nullptr) return 0;
+    uint64_t bits = 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const long long t = t0 - (K - 1) + 32 * w + (threadIdx.x & 31);
+        const bool first = t >= 0 && t < T && __ldg(seg + t) == 0;
+        bits |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, first)) << (32 * w);
+    }
+    return bits;
+}
+// Whether tap k of token i of the walk counts: no start at tokens i-k+1 .. i.
+template <int K> __device__ __forceinline__ bool conv_counts(uint64_t starts, int i, int k) {
+    return ((starts >> (i + K - k)) & ((1u << k) - 1u)) == 0;
+}
+// Whether all taps of tokens i .. i+n-1 do.
+template <int K> __device__ __forceinline__ bool conv_clear(uint64_t starts, int i, int n) {
+    return ((starts >> (i + 1)) & ((1ull << (n + K - 2)) - 1ull)) == 0;
+}
 
 template <class St, int V> __device__ __forceinline__ void conv_load(const St *p, bool in, float (&x)[V]) {
     if (in) {
@@ -48,59 +76,64 @@ __device__ __forceinline__ void conv_token(const ConvArgs &a, long long b, long 
         conv_load<St, V>(static_cast<const St *>(a.x0) + (b * (K - 1) + t + (K - 1)) * a.D + d, in && a.x0 != nullptr, x);
 }
 
-template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit) conv_fwd_kernel(const ConvArgs a) {
+// Up to N tokens from token i of the walk on; CLEAR: all taps count, and all N
+// are there.
+template <class St, int V, int K, int N, bool CLEAR>
+__device__ __forceinline__ void conv_fwd_tokens(const typename RawOf<St, V>::T (&raw)[N], int i, int n, uint64_t starts,
+                                                const float (&w)[K][V], const float (&bias)[V], float (&hist)[K - 1][V],
+                                                St *out, long long stride) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (!CLEAR && j >= n) break;
+        float x[V], y[V];
+        widen_raw(raw[j], x);
+        vfma<V>(y, w[0], x, bias);
+#pragma unroll
+        for (int k = 1; k < K; ++k)
+            if (CLEAR || conv_counts<K>(starts, i + j, k)) vfma<V>(y, w[k], hist[k - 1], y);
+        store_lanes<St, V>(out + j * stride, y);
+#pragma unroll
+        for (int k = K - 2; k > 0; --k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) hist[k][v] = hist[k - 1][v];
+#pragma unroll
+        for (int v = 0; v < V; ++v) hist[0][v] = x[v];
+    }
+}
+
+template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 ? 1 : 2) conv_fwd_kernel(const ConvArgs a) {
+    constexpr int N = ConvAhead<St, V, 1>::tokens;
     const unsigned lanes = blockIdx.x % a.ndt, chunk = blockIdx.x / a.ndt;
     const long long b = blockIdx.y;
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
     const long long t0 = (static_cast<long long>(chunk) * kConvSplit + threadIdx.y) * kConvSteps;
-    if (d >= a.D || t0 >= a.T) return;
+    if (t0 >= a.T) return;
+    const uint64_t starts = conv_starts<K>(a.seg ? a.seg + b * a.T : nullptr, t0, a.T);
+    if (d >= a.D) return;
     const int n = static_cast<int>(a.T - t0 < kConvSteps ? a.T - t0 : kConvSteps);
+    const St *xp = static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d;
+    St *op = static_cast<St *>(a.o.p) + b * a.o.sb + t0 * a.o.st + d;
     float w[K][V], bias[V], hist[K - 1][V];  // hist[k]: x_{t-1-k}; w[k]: the tap of x_{t-k}
+    typename RawOf<St, V>::T raw[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) raw[j] = conv_raw<St, V>(xp + j * a.x.st, j < n);
+#pragma unroll
+    for (int k = K - 2; k >= 0; --k) conv_token<St, V, K>(a, b, t0 - 1 - k, d, true, hist[k]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int k = 0; k < K; ++k) w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
         bias[v] = a.bias ? __ldg(a.bias + d + v) : 0.0f;
     }
-    const int32_t *seg = a.seg ? a.seg + b * a.T : nullptr;
-    int run = K - 1;
+    for (int i = 0; i < n; i += N) {
+        if (i > 0) {
 #pragma unroll
-    for (int k = K - 2; k >= 0; --k) {
-        const long long t = t0 - 1 - k;
-        conv_token<St, V, K>(a, b, t, d, true, hist[k]);
-        run = seg && t >= 0 && __ldg(seg + t) == 0 ? 0 : (run < K - 1 ? run + 1 : K - 1);
-    }
-    const St *xp = static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d;
-    St *op = static_cast<St *>(a.o.p) + b * a.o.sb + t0 * a.o.st + d;
-    for (int j0 = 0; j0 < n; j0 += kConvAhead) {
-        typename RawOf<St, V>::T xr[kConvAhead];
-        int first[kConvAhead];
-#pragma unroll
-        for (int j = 0; j < kConvAhead; ++j) {
-            xr[j] = conv_raw<St, V>(xp + (j0 + j) * a.x.st, j0 + j < n);
-            first[j] = seg && j0 + j < n ? __ldg(seg + t0 + j0 + j) : 1;
+            for (int j = 0; j < N; ++j) raw[j] = conv_raw<St, V>(xp + (i + j) * a.x.st, i + j < n);
         }
-#pragma unroll
-        for (int j = 0; j < kConvAhead; ++j) {
-            if (j0 + j >= n) break;
-            run = first[j] == 0 ? 0 : (run < K - 1 ? run + 1 : K - 1);
-            float x[V], y[V];
-            widen_raw(xr[j], x);
-#pragma unroll
-            for (int v = 0; v < V; ++v) y[v] = __fmaf_rn(w[0][v], x[v], bias[v]);
-#pragma unroll
-            for (int k = 1; k < K; ++k)
-                if (k <= run)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] = __fmaf_rn(w[k][v], hist[k - 1][v], y[v]);
-            store_lanes<St, V>(op + (j0 + j) * a.o.st, y);
-#pragma unroll
-            for (int k = K - 2; k > 0; --k)
-#pragma unroll
-                for (int v = 0; v < V; ++v) hist[k][v] = hist[k - 1][v];
-#pragma unroll
-            for (int v = 0; v < V; ++v) hist[0][v] = x[v];
-        }
+        if (i + N <= n && conv_clear<K>(starts, i, N))
+            conv_fwd_tokens<St, V, K, N, true>(raw, i, N, starts, w, bias, hist, op + i * a.o.st, a.o.st);
+        else
+            conv_fwd_tokens<St, V, K, N, false>(raw, i, n - i, starts, w, bias, hist, op + i * a.o.st, a.o.st);
     }
     if (a.last != nullptr && t0 + n == a.T) {
         St *to = static_cast<St *>(a.last) + b * (K - 1) * a.D + d;
@@ -109,108 +142,120 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
     }
 }
 
-// A walk adds grad_out_t's part to the gradients of tokens t .. t-K+1, which it
-// holds until they are complete; it reads K - 1 tokens of grad_out past its
-// own for them.  The walk at token 0 holds the tokens of x0 too.
-template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, 2) conv_bwd_kernel(const ConvArgs a) {
+// What a backward walk holds: taps, the sums of grad_w and grad_bias, the last
+// tokens, and held[k], the gradient of token t-k so far.
+template <int V, int K> struct ConvWalk {
+    float w[K][V], gw[K][V], gb[V], hist[K - 1][V], held[K][V];
+};
+
+// Tokens i .. i+N-1 of the walk add their parts to the gradients of the K tokens
+// up to each of them; the one that is complete goes out.  CLEAR: all N are the
+// walk's own, all taps count, all complete tokens are the walk's own and no
+// gradient comes in at them.
+template <class St, int V, int K, int N, bool CLEAR>
+__device__ __forceinline__ void conv_bwd_tokens(const ConvArgs &a, const typename RawOf<St, V>::T (&xr)[N],
+                                                const typename RawOf<St, V>::T (&gr)[N], int i, int n, long long t0,
+                                                uint64_t starts, ConvWalk<V, K> &c, St *out, St *out0, const St *gl) {
+    const long long tail = a.T - (K - 1);  // the first token of `last`
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (!CLEAR && i + j >= n + K - 1) break;
+        const long long t = t0 + i + j;
+        float x[V], g[V];
+        widen_raw(xr[j], x);
+        widen_raw(gr[j], g);
+#pragma unroll
+        for (int k = K - 1; k > 0; --k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) c.held[k][v] = c.held[k - 1][v];
+        if (CLEAR) {
+            vmul<V>(c.held[0], c.w[0], g);
+#pragma unroll
+            for (int k = 1; k < K; ++k) vfma<V>(c.held[k], c.w[k], g, c.held[k]);
+        } else {
+            conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < a.T && t >= tail, c.held[0]);
+            if (t < a.T)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (k == 0 || conv_counts<K>(starts, i + j, k)) vfma<V>(c.held[k], c.w[k], g, c.held[k]);
+        }
+        if (CLEAR || i + j < n) {
+            vadd<V>(c.gb, c.gb, g);
+            vfma<V>(c.gw[0], g, x, c.gw[0]);
+#pragma unroll
+            for (int k = 1; k < K; ++k)
+                if (CLEAR || conv_counts<K>(starts, i + j, k)) vfma<V>(c.gw[k], g, c.hist[k - 1], c.gw[k]);
+#pragma unroll
+            for (int k = K - 2; k > 0; --k)
+#pragma unroll
+                for (int v = 0; v < V; ++v) c.hist[k][v] = c.hist[k - 1][v];
+#pragma unroll
+            for (int v = 0; v < V; ++v) c.hist[0][v] = x[v];
+        }
+        const long long done = t - (K - 1);  // complete now
+        if (CLEAR || done >= t0)
+            store_lanes<St, V>(out + (i + j - (K - 1)) * a.o.st, c.held[K - 1]);
+        else if (done < 0 && a.grad_x0 != nullptr && done >= -(K - 1))
+            store_lanes<St, V>(out0 + (done + (K - 1)) * a.D, c.held[K - 1]);
+    }
+}
+
+// A walk reads K - 1 tokens of grad_out past its own, for the gradients of its
+// last tokens.  The walk at token 0 holds the tokens of x0 too.
+template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 && V > 1 ? 1 : 2) conv_bwd_kernel(const ConvArgs a) {
+    constexpr int N = ConvAhead<St, V, 2>::tokens;
     __shared__ float sums[kConvSplit][K + 1][32 * V];
     const unsigned lanes = blockIdx.x % a.ndt, chunk = blockIdx.x / a.ndt;
     const long long b = blockIdx.y;
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
     const long long t0 = (static_cast<long long>(chunk) * kConvSplit + threadIdx.y) * kConvSteps;
-    const bool in = d < a.D;
-    float gw[K][V], gb[V];
+    ConvWalk<V, K> c;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        gb[v] = 0.0f;
+        c.gb[v] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) gw[k][v] = 0.0f;
+        for (int k = 0; k < K; ++k) c.gw[k][v] = 0.0f;
     }
-    if (in && t0 < a.T) {
+    const uint64_t starts = t0 < a.T ? conv_starts<K>(a.seg ? a.seg + b * a.T : nullptr, t0, a.T) : 0;
+    if (d < a.D && t0 < a.T) {
         const int n = static_cast<int>(a.T - t0 < kConvSteps ? a.T - t0 : kConvSteps);
-        float w[K][V], hist[K - 1][V], held[K][V];  // held[k]: gradient of token t-k so far
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int k = 0; k < K; ++k) w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
-        const int32_t *seg = a.seg ? a.seg + b * a.T : nullptr;
-        const St *gl = static_cast<const St *>(a.grad_last) + b * (K - 1) * a.D + d;
-        const long long tail = a.T - (K - 1);  // the first token of `last`
-        int run = K - 1;
-#pragma unroll
-        for (int k = K - 2; k >= 0; --k) {
-            const long long t = t0 - 1 - k;
-            conv_token<St, V, K>(a, b, t, d, true, hist[k]);
-            run = seg && t >= 0 && __ldg(seg + t) == 0 ? 0 : (run < K - 1 ? run + 1 : K - 1);
-            // tokens before token 0 that are still among the last ones
-            conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < 0 && t >= tail, held[k]);
-        }
+        const long long left = a.T - t0, tail = a.T - (K - 1);
         const St *xp = static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d;
         const St *gp = static_cast<const St *>(a.go.p) + b * a.go.sb + t0 * a.go.st + d;
-        St *op = static_cast<St *>(a.o.p) + b * a.o.sb + d;
+        const St *gl = static_cast<const St *>(a.grad_last) + b * (K - 1) * a.D + d;
+        St *op = static_cast<St *>(a.o.p) + b * a.o.sb + t0 * a.o.st + d;
         St *o0 = static_cast<St *>(a.grad_x0) + b * (K - 1) * a.D + d;
-        const long long left = a.T - t0;
-        for (int j0 = 0; j0 < n + K - 1; j0 += kConvAhead) {
-            typename RawOf<St, V>::T xr[kConvAhead], gr[kConvAhead];
-            int first[kConvAhead];
+        typename RawOf<St, V>::T xr[N], gr[N];
+        for (int i = 0; i < n + K - 1; i += N) {
 #pragma unroll
-            for (int j = 0; j < kConvAhead; ++j) {
-                const bool there = j0 + j < n + K - 1 && j0 + j < left;
-                xr[j] = conv_raw<St, V>(xp + (j0 + j) * a.x.st, j0 + j < n);
-                gr[j] = conv_raw<St, V>(gp + (j0 + j) * a.go.st, there);
-                first[j] = seg && there ? __ldg(seg + t0 + j0 + j) : 1;
+            for (int j = 0; j < N; ++j) {
+                xr[j] = conv_raw<St, V>(xp + (i + j) * a.x.st, i + j < n);
+                gr[j] = conv_raw<St, V>(gp + (i + j) * a.go.st, i + j < n + K - 1 && i + j < left);
             }
+            if (i == 0) {
 #pragma unroll
-            for (int j = 0; j < kConvAhead; ++j) {
-                if (j0 + j >= n + K - 1) break;
-                const long long t = t0 + j0 + j;
-                float x[V], g[V];
-                widen_raw(xr[j], x);
-                widen_raw(gr[j], g);
-                run = first[j] == 0 ? 0 : (run < K - 1 ? run + 1 : K - 1);
-#pragma unroll
-                for (int k = K - 1; k > 0; --k)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) held[k][v] = held[k - 1][v];
-                conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < a.T && t >= tail, held[0]);
-                if (t < a.T) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (k == 0 || k <= run)
-#pragma unroll
-                            for (int v = 0; v < V; ++v) held[k][v] = __fmaf_rn(w[k][v], g[v], held[k][v]);
-                    if (j0 + j < n) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            gb[v] += g[v];
-                            gw[0][v] = __fmaf_rn(g[v], x[v], gw[0][v]);
-                        }
-#pragma unroll
-                        for (int k = 1; k < K; ++k)
-                            if (k <= run)
-#pragma unroll
-                                for (int v = 0; v < V; ++v) gw[k][v] = __fmaf_rn(g[v], hist[k - 1][v], gw[k][v]);
-#pragma unroll
-                        for (int k = K - 2; k > 0; --k)
-#pragma unroll
-                            for (int v = 0; v < V; ++v) hist[k][v] = hist[k - 1][v];
-#pragma unroll
-                        for (int v = 0; v < V; ++v) hist[0][v] = x[v];
-                    }
+                for (int k = K - 2; k >= 0; --k) {
+                    const long long t = t0 - 1 - k;
+                    conv_token<St, V, K>(a, b, t, d, true, c.hist[k]);
+                    // tokens before token 0 that are still among the last ones
+                    conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < 0 && t >= tail, c.held[k]);
                 }
-                const long long done = t - (K - 1);  // complete now
-                if (done >= t0)
-                    store_lanes<St, V>(op + done * a.o.st, held[K - 1]);
-                else if (done < 0 && a.grad_x0 != nullptr && done >= -(K - 1))
-                    store_lanes<St, V>(o0 + (done + (K - 1)) * a.D, held[K - 1]);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int k = 0; k < K; ++k) c.w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
             }
+            if (i >= K - 1 && i + N <= n && conv_clear<K>(starts, i, N) && (a.grad_last == nullptr || t0 + i + N <= tail))
+                conv_bwd_tokens<St, V, K, N, true>(a, xr, gr, i, n, t0, starts, c, op, o0, gl);
+            else
+                conv_bwd_tokens<St, V, K, N, false>(a, xr, gr, i, n, t0, starts, c, op, o0, gl);
         }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) sums[threadIdx.y][K - 1 - k][threadIdx.x + 32 * v] = gw[k][v];
-        sums[threadIdx.y][K][threadIdx.x + 32 * v] = gb[v];
+        for (int k = 0; k < K; ++k) sums[threadIdx.y][K - 1 - k][threadIdx.x + 32 * v] = c.gw[k][v];
+        sums[threadIdx.y][K][threadIdx.x + 32 * v] = c.gb[v];
     }
     __syncthreads();
     float *part = a.part + (b * a.chunks + chunk) * (K + 1) * a.D;

@@ -22,12 +22,13 @@ struct EmbedArgs {
     int sm_count;
     // backward scratch
     uint32_t *keys[2], *vals[2];  // [N]: token ids (V: none) and token numbers
-    uint32_t *totals;             // [passes][kSortCtas][kSortBins]
-    uint8_t *present;             // [V]
+    int *runs;                    // long runs, and where each starts [N / kLongRun]
+    uint32_t *run_at;
     float *part;                  // [blocks][2][D]
     int bits;                     // of a digit
     int passes;
-    int per;                      // sorted tokens a CTA sums
+    int per;                      // sorted tokens of a stretch
+    int held;                     // tokens of a CTA that the sort keeps on chip, or 0
 };
 
 constexpr int kSortCtas = 8;      // one cluster

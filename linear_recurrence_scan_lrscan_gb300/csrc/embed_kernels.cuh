@@ -3,14 +3,15 @@
 // with ids[n] = v, in the order of the tokens (two calls agree bit for bit).
 // A negative id is no token: a row of zeros, and no gradient.
 //
-// Backward in three kernels.  One cluster sorts the tokens by id, stably, by
-// digits of up to 9 bits: each warp counts the digits of its own stretch of
-// tokens, the counts become every warp's first places, and the warp moves its
-// tokens there.  Then CTAs sum the rows of equal stretches of the sorted
-// tokens, whatever ids they hold, so that a frequent id takes many CTAs and a
-// rare one shares its CTA; other CTAs of the same launch write the zeros of
-// the rows that have no token.  A stretch's first and last ids may go on
-// outside it: those sums are left in fp32, and the third kernel adds them up.
+// Backward in three kernels.  In the first, one cluster sorts the tokens by id,
+// stably, by digits of up to 9 bits: each warp counts the digits of its own
+// stretch of tokens, the counts become every warp's first places, and the warp
+// moves its tokens there.  Meanwhile the other CTAs write the zeros of the rows
+// that have no token, most of what is written for a large table; each finds its
+// rows' tokens by reading all ids once.  In the second, CTAs sum the rows of
+// equal stretches of the sorted tokens.  A run of one id is summed by the CTA it
+// starts in, up to 64 tokens past its stretch; a longer run takes every CTA it
+// touches, which leave fp32 sums, and the third kernel adds those up.
 #pragma once
 
 #include "embed_args.h"
@@ -29,7 +30,7 @@ __device__ __forceinline__ void report_id(const EmbedArgs &a, long long n) {
     }
 }
 
-// Eight (or one) lanes.
+// V lanes of a row; eight fp32 lanes are two 16-byte loads.
 template <class St, int V> __device__ __forceinline__ void row_load(const St *p, float (&x)[V]) {
     if constexpr (V == 8 && std::is_same<St, float>::value) {
         const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
@@ -73,10 +74,19 @@ template <class W, class O, int V, int R> __global__ void __launch_bounds__(256)
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+// Shared memory of another CTA of the cluster.
+__device__ __forceinline__ uint32_t remote(const void *p, unsigned rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
     return r;
+}
+__device__ __forceinline__ void remote_store(uint32_t at, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t remote_load(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
 // Lanes of the warp that hold the same digit, `bits` bits long.
@@ -90,57 +100,151 @@ __device__ __forceinline__ unsigned same_digit(unsigned digit, int bits) {
     return peers;
 }
 
-// Sorts (id, token number) by id, stably; marks the ids that occur.
+constexpr int kSortAhead = 8;        // tokens of a lane in flight
+constexpr int kZeroSpan = 32768;     // rows whose tokens a zeroing CTA looks for at once
+constexpr int kZeroBytes = 4096;     // most bytes of a bulk copy of zeros
+
+// Bulk copy shared -> global: both on 16-byte boundaries, bytes a multiple of 16.
+__device__ __forceinline__ void bulk_store(void *to, const void *from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_addr(from)), "r"(bytes)
+                 : "memory");
+}
+
+// The rows v0 .. v1-1 of the table that no token has: zeros.  Rows on 16-byte
+// boundaries (V > 1) leave as bulk copies of a block of zeros.
+template <class O, int V>
+__device__ __forceinline__ void embed_zero_rows(const EmbedArgs &a, long long v0, long long v1, uint32_t *bits) {
+    __shared__ alignas(16) uint4 zeros[V > 1 ? kZeroBytes / 16 : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if constexpr (V > 1) {
+        for (int j = threadIdx.x; j < kZeroBytes / 16; j += blockDim.x) zeros[j] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    for (long long first = v0; first < v1; first += kZeroSpan) {
+        const int span = static_cast<int>(v1 - first < kZeroSpan ? v1 - first : kZeroSpan);
+        for (int j = threadIdx.x; j < (span + 31) / 32; j += blockDim.x) bits[j] = 0;
+        __syncthreads();
+        for (long long n0 = threadIdx.x; n0 < a.N; n0 += kSortAhead * blockDim.x) {
+            long long id[kSortAhead];
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k) {
+                const long long n = n0 + static_cast<long long>(k) * blockDim.x;
+                id[k] = n < a.N ? token_id(a, n) - first : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k)
+                if (id[k] >= 0 && id[k] < span) atomicOr(bits + id[k] / 32, 1u << (id[k] % 32));
+        }
+        __syncthreads();
+        for (int r = warp; r < span; r += warps) {
+            if (bits[r / 32] >> (r % 32) & 1u) continue;
+            O *row = static_cast<O *>(a.out) + (first + r) * a.D;
+            if constexpr (V > 1) {
+                const long long bytes = a.D * static_cast<long long>(sizeof(O));
+                if (lane == 0)
+                    for (long long at = 0; at < bytes; at += kZeroBytes)
+                        bulk_store(reinterpret_cast<char *>(row) + at, zeros,
+                                   static_cast<uint32_t>(bytes - at < kZeroBytes ? bytes - at : kZeroBytes));
+            } else {
+                const float zero[1] = {0.0f};
+                for (long long d = lane; d < a.D; d += 32) store_lanes<O, 1>(row + d, zero);
+            }
+        }
+        __syncthreads();
+    }
+    if constexpr (V > 1) {
+        bulk_commit();
+        bulk_wait<0>();
+    }
+}
+
+// The first cluster sorts (id, token number) by id, stably; the others write
+// zeros.  While the zeros take the memory's bandwidth a round trip to it is slow,
+// so the tokens between two passes stay in the cluster's shared memory where
+// they fit (`a.held` tokens a CTA; 0: in memory).
+template <class O, int V>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortWarps * 32, 1)
 embed_sort_kernel(const EmbedArgs a) {
-    extern __shared__ uint32_t count[];  // [kSortWarps][bins + 1]: a warp's counts, then its next places
-    __shared__ uint32_t base[kSortBins];
+    extern __shared__ uint32_t count[];  // [kSortWarps][bins + 1]: a warp's counts, then its next places;
+                                         // then the tokens held: [2] x [key, val] x [a.held]
+    __shared__ uint32_t base[kSortBins], totals[kSortBins];
     __shared__ uint32_t sums[kSortBins / 32];
+    if (blockIdx.x >= kSortCtas) {
+        const long long ctas = gridDim.x - kSortCtas, me = blockIdx.x - kSortCtas;
+        const long long each = (a.V + ctas - 1) / ctas, v0 = me * each;
+        embed_zero_rows<O, V>(a, v0 < a.V ? v0 : a.V, v0 + each < a.V ? v0 + each : a.V, count);
+        return;
+    }
     const int bins = 1 << a.bits, row = bins + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned rank = cluster_rank();
+    const unsigned rank = blockIdx.x;
     const long long stretch = ((a.N + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
     const long long first = (static_cast<long long>(rank) * kSortWarps + warp) * stretch;
     const long long last = first + stretch < a.N ? first + stretch : a.N;
-    for (long long v = rank * blockDim.x + threadIdx.x; v < a.V; v += kSortCtas * blockDim.x) a.present[v] = 0;
+    const bool keep = stretch <= 32 * kSortAhead;  // the keys counted are still in registers when they move
+    uint32_t *store = count + kSortWarps * row;
+    const unsigned held = static_cast<unsigned>(a.held);
+    if (rank == 0 && threadIdx.x == 0) *a.runs = 0;
     uint32_t *mine = count + warp * row;
     for (int p = 0; p < a.passes; ++p) {
         const uint32_t *kin = p & 1 ? a.keys[1] : a.keys[0], *vin = p & 1 ? a.vals[1] : a.vals[0];
         uint32_t *kout = p & 1 ? a.keys[0] : a.keys[1], *vout = p & 1 ? a.vals[0] : a.vals[1];
         const int shift = p * a.bits;
-        auto key_of = [&](long long n) -> uint32_t {
-            if (p > 0) return kin[n];
-            const long long id = token_id(a, n);
-            if (id >= a.V) report_id(a, n);
-            return id >= 0 && id < a.V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(a.V);
+        uint32_t key[kSortAhead], val[kSortAhead];
+        auto load = [&](long long n0) {
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k) {
+                const long long n = n0 + 32 * k + lane;
+                key[k] = val[k] = 0;
+                if (n >= last) continue;
+                if (p > 0 && held > 0) {
+                    const uint32_t *from = store + (p & 1) * 2 * held + (n - static_cast<long long>(rank) * kSortWarps * stretch);
+                    key[k] = from[0];
+                    val[k] = from[held];
+                } else if (p > 0) {
+                    key[k] = kin[n];
+                    val[k] = vin[n];
+                } else {
+                    const long long id = token_id(a, n);
+                    if (id >= a.V) report_id(a, n);
+                    key[k] = id >= 0 && id < a.V ? static_cast<uint32_t>(id) : static_cast<uint32_t>(a.V);
+                    val[k] = static_cast<uint32_t>(n);
+                }
+            }
         };
         for (int j = threadIdx.x; j < kSortWarps * row; j += blockDim.x) count[j] = 0;
         __syncthreads();
-        for (long long n0 = first; n0 < last; n0 += 32) {
-            const bool there = n0 + lane < last;
-            // lanes past the end hold the last digit, and do not count
-            const unsigned digit = there ? (key_of(n0 + lane) >> shift) & (bins - 1) : bins - 1;
-            const unsigned live = __ballot_sync(0xffffffffu, there);
-            const unsigned peers = same_digit(digit, a.bits) & live;
-            if (there && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
-            __syncwarp();
+        for (long long n0 = first; n0 < last; n0 += 32 * kSortAhead) {
+            load(n0);
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k) {
+                if (n0 + 32 * k >= last) break;
+                // lanes past the end hold the last digit, and do not count
+                const bool there = n0 + 32 * k + lane < last;
+                const unsigned digit = there ? (key[k] >> shift) & (bins - 1) : bins - 1;
+                const unsigned live = __ballot_sync(0xffffffffu, there);
+                const unsigned peers = same_digit(digit, a.bits) & live;
+                if (there && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
+                __syncwarp();
+            }
         }
         __syncthreads();
-        uint32_t *totals = a.totals + (static_cast<size_t>(p) * kSortCtas) * kSortBins;
         for (int j = threadIdx.x; j < bins; j += blockDim.x) {  // a digit's count, and each warp's share before it
             uint32_t t = 0;
+#pragma unroll 8
             for (int w = 0; w < kSortWarps; ++w) {
                 const uint32_t c = count[w * row + j];
                 count[w * row + j] = t;
                 t += c;
             }
-            totals[rank * kSortBins + j] = t;
+            totals[j] = t;
         }
         cluster_barrier();
         if (threadIdx.x < bins) {  // whole warps: bins is 32 at least
             uint32_t all = 0, before = 0;
+#pragma unroll
             for (unsigned r = 0; r < kSortCtas; ++r) {
-                const uint32_t t = __ldcg(totals + r * kSortBins + threadIdx.x);
+                const uint32_t t = remote_load(remote(totals + threadIdx.x, r));
                 before += r < rank ? t : 0;
                 all += t;
             }
@@ -159,21 +263,31 @@ embed_sort_kernel(const EmbedArgs a) {
             base[threadIdx.x] += add;
         }
         __syncthreads();
-        for (long long n0 = first; n0 < last; n0 += 32) {
-            const bool there = n0 + lane < last;
-            const uint32_t key = there ? key_of(n0 + lane) : 0;
-            const unsigned digit = there ? (key >> shift) & (bins - 1) : bins - 1;
-            const unsigned live = __ballot_sync(0xffffffffu, there);
-            const unsigned peers = same_digit(digit, a.bits) & live;
-            if (there) {
-                const uint32_t at = base[digit] + mine[digit] + __popc(peers & ((1u << lane) - 1u));
-                kout[at] = key;
-                vout[at] = p > 0 ? vin[n0 + lane] : static_cast<uint32_t>(n0 + lane);
-                if (p + 1 == a.passes && key < a.V) a.present[key] = 1;
+        for (long long n0 = first; n0 < last; n0 += 32 * kSortAhead) {
+            if (!keep) load(n0);
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k) {
+                if (n0 + 32 * k >= last) break;
+                const bool there = n0 + 32 * k + lane < last;
+                const unsigned digit = there ? (key[k] >> shift) & (bins - 1) : bins - 1;
+                const unsigned live = __ballot_sync(0xffffffffu, there);
+                const unsigned peers = same_digit(digit, a.bits) & live;
+                if (there) {
+                    const uint32_t at = base[digit] + mine[digit] + __popc(peers & ((1u << lane) - 1u));
+                    if (p + 1 < a.passes && held > 0) {
+                        const unsigned whose = at / held;
+                        uint32_t *to = store + ((p + 1) & 1) * 2 * held + (at - whose * held);
+                        remote_store(remote(to, whose), key[k]);
+                        remote_store(remote(to + held, whose), val[k]);
+                    } else {
+                        kout[at] = key[k];
+                        vout[at] = val[k];
+                    }
+                }
+                __syncwarp();
+                if (there && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
+                __syncwarp();
             }
-            __syncwarp();
-            if (there && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
-            __syncwarp();
         }
         cluster_barrier();  // the tokens are where the next pass reads them
     }
@@ -186,15 +300,7 @@ __device__ __forceinline__ void put_row(const EmbedArgs &a, long long id, long l
     for (int v = 0; v < V; ++v) x[v] *= a.scale;
     if (a.add) {
         float y[V];
-        if constexpr (V == 8 && std::is_same<O, float>::value) {
-            float u[4], w[4];
-            unpack_lanes<O, 4>(to, u);
-            unpack_lanes<O, 4>(to + 4, w);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) { y[v] = u[v]; y[v + 4] = w[v]; }
-        } else {
-            unpack_lanes<O, V>(to, y);
-        }
+        unpack_lanes<O, V>(to, y);
 #pragma unroll
         for (int v = 0; v < V; ++v) x[v] += y[v];
     }
@@ -202,77 +308,92 @@ __device__ __forceinline__ void put_row(const EmbedArgs &a, long long id, long l
 }
 
 constexpr int kSumAhead = 8;     // rows in flight a thread
-constexpr int kMostPer = 32;     // most sorted tokens a CTA sums
-constexpr int kZeroRows = 32;    // rows of the table a zeroing CTA looks at
+constexpr int kMostPer = 32;     // most sorted tokens of a stretch
+constexpr int kLongRun = 64;     // a run of more tokens than this is shared
 
-template <class G, class O, int V> __global__ void __launch_bounds__(512) embed_sum_kernel(const EmbedArgs a, int blocks) {
-    const long long d = (static_cast<long long>(blockIdx.y) * blockDim.x + threadIdx.x) * V;
-    if (blockIdx.x >= blocks) {  // rows without a token
-        if (d >= a.D) return;
-        const long long v0 = static_cast<long long>(blockIdx.x - blocks) * kZeroRows;
-        float zero[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) zero[v] = 0.0f;
-        for (int r = 0; r < kZeroRows && v0 + r < a.V; ++r)
-            if (!a.present[v0 + r]) store_lanes<O, V>(static_cast<O *>(a.out) + (v0 + r) * a.D + d, zero);
-        return;
-    }
-    __shared__ uint32_t key[kMostPer + 2], val[kMostPer];
+template <class G, class O, int V> __global__ void __launch_bounds__(512) embed_sum_kernel(const EmbedArgs a) {
+    // the sorted tokens from kLongRun before the stretch to kLongRun after it
+    __shared__ uint32_t key[kMostPer + 2 * kLongRun + 1], val[kMostPer + kLongRun];
+    __shared__ int from, to;
+    pdl_wait();
     const uint32_t *keys = a.passes & 1 ? a.keys[1] : a.keys[0], *vals = a.passes & 1 ? a.vals[1] : a.vals[0];
     const uint32_t none = static_cast<uint32_t>(a.V);
     const long long j0 = static_cast<long long>(blockIdx.x) * a.per;
     const int n = static_cast<int>(a.N - j0 < a.per ? a.N - j0 : a.per);
-    for (int j = threadIdx.x; j < n + 2; j += blockDim.x) {  // and the ids on both sides
-        const long long at = j0 + j - 1;
+    const long long d = (static_cast<long long>(blockIdx.y) * blockDim.x + threadIdx.x) * V;
+    for (int j = threadIdx.x; j < n + 2 * kLongRun + 1; j += blockDim.x) {
+        const long long at = j0 + j - kLongRun;
         key[j] = at >= 0 && at < a.N ? keys[at] : none;
-        if (j < n) val[j] = vals[j0 + j];
+        if (j < n + kLongRun) val[j] = j0 + j < a.N ? vals[j0 + j] : 0;
+    }
+    __syncthreads();
+    const uint32_t *mid = key + kLongRun;  // mid[i]: the id of sorted token j0 + i
+    if (threadIdx.x < 32) {
+        // Which tokens this CTA sums.  The run that comes in: the stretch's
+        // share of it if it is long, else none of it.  The run that goes out:
+        // the stretch's share if it is long, else all of it.
+        const int lane = threadIdx.x;
+        int back = 0, on = 0, tail = 0;  // tokens of the first run before the stretch and in or after it; of the last run
+        for (int k = 1; k <= kLongRun; k += 32) back += __popc(__ballot_sync(0xffffffffu, mid[-k - lane] == mid[0]));
+        for (int k = 0; k < n + kLongRun; k += 32) {
+            const int i = k + lane;
+            on += __popc(__ballot_sync(0xffffffffu, i < n + kLongRun && mid[i] == mid[0]));
+            tail += __popc(__ballot_sync(0xffffffffu, i < n + kLongRun && mid[i] == mid[n - 1]));
+        }
+        if (lane == 0) {
+            const bool comes = back > 0, whole = on >= n;  // whole: one id all through
+            int f = 0, t = n;
+            if (mid[0] == none) t = 0;
+            else {
+                const bool long_in = back + on > kLongRun;
+                if (comes && !long_in) f = on < n ? on : n;
+                int start = 0;  // where the last run starts, if in the stretch
+                while (start < n && mid[start] != mid[n - 1]) ++start;
+                const bool goes = mid[n] == mid[n - 1] && mid[n - 1] != none;
+                const bool starts = !whole || !comes;
+                if (goes && starts) {
+                    if (tail > kLongRun) {  // long: its share, and the run is put down for the third kernel
+                        if (blockIdx.y == 0) a.run_at[atomicAdd(a.runs, 1)] = static_cast<uint32_t>(j0 + start);
+                    } else {
+                        t = start + tail;
+                    }
+                }
+                if (whole && comes && !long_in) t = f;  // another CTA's
+            }
+            from = f;
+            to = t;
+        }
     }
     __syncthreads();
     if (d >= a.D) return;
     const G *rows = static_cast<const G *>(a.in) + d;
+    const int last = to;
     float sum[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-    bool opened = key[0] != key[1];  // the current id starts in this stretch
-    for (int i0 = 0; i0 < n; i0 += kSumAhead) {
-        typename RawOf<G, std::is_same<G, float>::value && V == 8 ? 4 : V>::T raw[kSumAhead][std::is_same<G, float>::value && V == 8 ? 2 : 1];
+    bool opened = mid[from] != mid[from - 1];  // the current id's run starts here
+    for (int i0 = from; i0 < last; i0 += kSumAhead) {
+        typename RawOf<G, V>::T raw[kSumAhead];
+#pragma unroll
+        for (int i = 0; i < kSumAhead; ++i)
+            if (i0 + i < last && mid[i0 + i] != none) raw[i] = load_raw<G, V>(rows + static_cast<long long>(val[i0 + i]) * a.D);
 #pragma unroll
         for (int i = 0; i < kSumAhead; ++i) {
-            if (i0 + i < n && key[i0 + i + 1] != none) {
-                const G *p = rows + static_cast<long long>(val[i0 + i]) * a.D;
-                if constexpr (std::is_same<G, float>::value && V == 8) {
-                    raw[i][0] = load_raw<G, 4>(p);
-                    raw[i][1] = load_raw<G, 4>(p + 4);
-                } else {
-                    raw[i][0] = load_raw<G, V>(p);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kSumAhead; ++i) {
-            if (i0 + i >= n) break;
-            const uint32_t id = key[i0 + i + 1];
+            if (i0 + i >= last) break;
+            const uint32_t id = mid[i0 + i];
             if (id == none) return;  // the tokens that are none come last
             float x[V];
-            if constexpr (std::is_same<G, float>::value && V == 8) {
-                float u[4], w[4];
-                widen_raw(raw[i][0], u);
-                widen_raw(raw[i][1], w);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) { x[v] = u[v]; x[v + 4] = w[v]; }
-            } else {
-                widen_raw(raw[i][0], x);
-            }
+            widen_raw(raw[i], x);
 #pragma unroll
             for (int v = 0; v < V; ++v) sum[v] += x[v];
-            const bool ends = key[i0 + i + 2] != id;
-            if (!ends && i0 + i + 1 < n) continue;
+            const bool ends = mid[i0 + i + 1] != id;
+            if (!ends && i0 + i + 1 < last) continue;
             if (ends && opened) {
                 put_row<O, V>(a, id, d, sum);
-            } else {  // goes on before (slot 0) or only after (slot 1) this stretch
-                float *to = a.part + (static_cast<long long>(blockIdx.x) * 2 + (opened ? 1 : 0)) * a.D + d;
+            } else {  // a long run's share: it came in (slot 0) or starts here (slot 1)
+                float *at = a.part + (static_cast<long long>(blockIdx.x) * 2 + (opened ? 1 : 0)) * a.D + d;
 #pragma unroll
-                for (int v = 0; v < V; ++v) to[v] = sum[v];
+                for (int v = 0; v < V; ++v) at[v] = sum[v];
             }
             opened = true;
 #pragma unroll
@@ -281,41 +402,41 @@ template <class G, class O, int V> __global__ void __launch_bounds__(512) embed_
     }
 }
 
-// An id that starts in stretch `blockIdx.x` and goes on in others: 32 columns a
-// CTA, whose eight warps take every eighth stretch.
+// The long runs, 32 columns a turn: the eight warps take every eighth stretch,
+// and their sums are added in warp order.
 template <class O> __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedArgs a) {
     __shared__ float sums[8][33];
+    pdl_wait();
     const uint32_t *keys = a.passes & 1 ? a.keys[1] : a.keys[0];
-    const long long j1 = (static_cast<long long>(blockIdx.x) + 1) * a.per;  // the next stretch
-    if (j1 >= a.N) return;
-    const uint32_t id = keys[j1];
-    if (id >= a.V || keys[j1 - 1] != id) return;
-    const long long j0 = j1 - a.per;
-    if (keys[j0] == id && j0 > 0 && keys[j0 - 1] == id) return;  // starts earlier
-    // the last stretch that holds the id, by bisection of the stretches' first ids
-    long long lo = blockIdx.x + 1, hi = (a.N + a.per - 1) / a.per;  // keys[lo * per] is the id, keys[hi * per] is not
-    while (hi - lo > 1) {
-        const long long mid = (lo + hi) / 2;
-        if (keys[mid * a.per] == id)
-            lo = mid;
-        else
-            hi = mid;
-    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long d = static_cast<long long>(blockIdx.y) * 32 + lane;
-    float sum = 0.0f;
-    if (d < a.D) {
-        if (warp == 0) sum = a.part[(static_cast<long long>(blockIdx.x) * 2 + 1) * a.D + d];
+    const long long columns = (a.D + 31) / 32, turns = static_cast<long long>(*a.runs) * columns;
+    for (long long turn = blockIdx.x; turn < turns; turn += gridDim.x) {
+        const long long at = a.run_at[turn / columns], first = at / a.per;
+        const uint32_t id = keys[at];
+        // the last stretch that starts inside the run: 256 stretches looked at together
+        const long long stretches = (a.N + a.per - 1) / a.per;
+        long long lo = first;
+        for (int more = 256; more == 256;) {
+            const long long j = lo + 1 + threadIdx.x;
+            more = __syncthreads_count(j < stretches && keys[j * a.per] == id);
+            lo += more;
+        }
+        const long long d = turn % columns * 32 + lane;
+        float sum = 0.0f;
+        if (d < a.D) {
+            if (warp == 0) sum = a.part[(first * 2 + 1) * a.D + d];
 #pragma unroll 8
-        for (long long j = blockIdx.x + 1 + warp; j <= lo; j += 8) sum += a.part[j * 2 * a.D + d];
-    }
-    sums[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && d < a.D) {
-        float x[1] = {0.0f};
+            for (long long j = first + 1 + warp; j <= lo; j += 8) sum += a.part[j * 2 * a.D + d];
+        }
+        sums[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0 && d < a.D) {
+            float x[1] = {0.0f};
 #pragma unroll
-        for (int w = 0; w < 8; ++w) x[0] += sums[w][lane];
-        put_row<O, 1>(a, id, d, x);
+            for (int w = 0; w < 8; ++w) x[0] += sums[w][lane];
+            put_row<O, 1>(a, id, d, x);
+        }
+        __syncthreads();
     }
 }
 

@@ -6,6 +6,10 @@
 namespace lrscan {
 namespace {
 
+// Lanes of a thread where rows fit wide accesses: 16 bytes of the wider type, so
+// that a warp's accesses have no gaps on either side.
+template <class A, class B> constexpr int kWide = 16 / (sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B));
+
 template <class W, class O, int V> int fwd(const EmbedArgs &a) {
     const long long nd = (a.D + 32 * V - 1) / (32 * V);
     const dim3 block(32, 8);
@@ -20,44 +24,61 @@ template <class W, class O, int V> int fwd(const EmbedArgs &a) {
     return cudaGetLastError() != cudaSuccess;
 }
 
-template <class G, class O, int V> int sums(const EmbedArgs &a) {
-    const long long lanes = (a.D + V - 1) / V;
-    const int threads = static_cast<int>(lanes >= 512 ? 512 : (lanes + 31) / 32 * 32);
-    const long long blocks = (a.N + a.per - 1) / a.per, zero = a.add ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
-    const long long ny = (lanes + threads - 1) / threads;
-    if (blocks + zero > 0x7fffffffLL || ny > 65535) return 1;
-    embed_sum_kernel<G, O, V><<<dim3(static_cast<unsigned>(blocks + zero), static_cast<unsigned>(ny)), threads, 0,
-                                a.stream>>>(a, static_cast<int>(blocks));
-    if (cudaGetLastError() != cudaSuccess) return 1;
-    if (blocks < 2) return 0;
-    embed_join_kernel<O><<<dim3(static_cast<unsigned>(blocks - 1), static_cast<unsigned>((a.D + 31) / 32)), 256, 0,
-                           a.stream>>>(a);
-    return cudaGetLastError() != cudaSuccess;
-}
-
-template <class G, class O> int bwd(const EmbedArgs &a) {
-    const int smem = kSortWarps * ((1 << a.bits) + 1) * 4;
-    static bool allowed[64] = {};
+template <class G, class O, int V> int bwd_vec(EmbedArgs a) {
+    constexpr int kMost = 212 * 1024;  // beside 8 KB that are static
+    static int fit[64] = {};  // clusters that run at once: fewer than SMs / 8, as a cluster stays within its part of the GPU
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    if (!allowed[dev]) {
-        if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSortWarps * (kSortBins + 1) * 4) != cudaSuccess)
+    if (fit[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kSortCtas);
+        cfg.blockDim = dim3(kSortWarps * 32);
+        cfg.dynamicSmemBytes = kMost;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kSortCtas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(embed_sort_kernel<O, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, embed_sort_kernel<O, V>, &cfg) != cudaSuccess)
             return 1;
-        allowed[dev] = true;
+        fit[dev] = n > 1 ? n : 2;
     }
-    embed_sort_kernel<<<kSortCtas, kSortWarps * 32, smem, a.stream>>>(a);
+    // one cluster sorts, the others write zeros
+    const int clusters = a.add ? 1 : fit[dev];
+    int smem = kSortWarps * ((1 << a.bits) + 1) * 4;
+    const long long stretch = ((a.N + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
+    const long long held = stretch * kSortWarps;  // tokens of a CTA
+    a.held = 0;
+    if (a.passes > 1 && smem + held * 16 <= kMost) {
+        a.held = static_cast<int>(held);
+        smem += static_cast<int>(held * 16);
+    }
+    embed_sort_kernel<O, V><<<clusters * kSortCtas, kSortWarps * 32, smem, a.stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return 1;
-    return a.vec ? sums<G, O, 8>(a) : sums<G, O, 1>(a);
+    const long long lanes = (a.D + V - 1) / V;
+    const long long ny = (lanes + 511) / 512;  // a row's lanes in equal parts
+    const int threads = static_cast<int>(((lanes + ny - 1) / ny + 31) / 32 * 32);
+    const long long blocks = (a.N + a.per - 1) / a.per;
+    if (blocks > 0x7fffffffLL || ny > 65535) return 1;
+    if (launch_pdl(embed_sum_kernel<G, O, V>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(ny)), dim3(threads), 0,
+                   a.stream, a) != cudaSuccess)
+        return 1;
+    if (a.N <= kLongRun) return 0;
+    return launch_pdl(embed_join_kernel<O>, dim3(8 * a.sm_count), dim3(256), 0, a.stream, a) != cudaSuccess;
 }
+
+template <class G, class O> int bwd(const EmbedArgs &a) { return a.vec ? bwd_vec<G, O, kWide<G, O>>(a) : bwd_vec<G, O, 1>(a); }
 
 }  // namespace
 
 int embed_fwd_launch(const EmbedArgs &a, int wdtype, int odtype) {
-    if (wdtype == 0 && odtype == 0) return a.vec ? fwd<float, float, 8>(a) : fwd<float, float, 1>(a);
-    if (wdtype == 0) return a.vec ? fwd<float, bf16_t, 8>(a) : fwd<float, bf16_t, 1>(a);
-    if (odtype == 0) return a.vec ? fwd<bf16_t, float, 8>(a) : fwd<bf16_t, float, 1>(a);
-    return a.vec ? fwd<bf16_t, bf16_t, 8>(a) : fwd<bf16_t, bf16_t, 1>(a);
+    if (wdtype == 0 && odtype == 0) return a.vec ? fwd<float, float, 16 / sizeof(float)>(a) : fwd<float, float, 1>(a);
+    if (wdtype == 0) return a.vec ? fwd<float, bf16_t, 16 / sizeof(bf16_t)>(a) : fwd<float, bf16_t, 1>(a);
+    if (odtype == 0) return a.vec ? fwd<bf16_t, float, 16 / sizeof(float)>(a) : fwd<bf16_t, float, 1>(a);
+    return a.vec ? fwd<bf16_t, bf16_t, 16 / sizeof(bf16_t)>(a) : fwd<bf16_t, bf16_t, 1>(a);
 }
 
 int embed_bwd_launch(const EmbedArgs &a, int gdtype, int wdtype) {

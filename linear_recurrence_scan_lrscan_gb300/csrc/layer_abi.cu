@@ -212,9 +212,9 @@ int copy_rows(void *dst, const void *src, size_t bytes, cudaStream_t st) {
 // Token embedding
 // ----------------------------------------------------------------------------
 struct EmbedScratch {
-    size_t list, totals, present, part;
+    size_t list, runs, part;
     int bits, passes, per;
-    size_t total() const { return 4 * list + totals + present + part; }
+    size_t total() const { return 4 * list + runs + part; }
 };
 EmbedScratch embed_scratch(int64_t N, int64_t V, int64_t D, int sm_count) {
     EmbedScratch s{};
@@ -227,8 +227,7 @@ EmbedScratch embed_scratch(int64_t N, int64_t V, int64_t D, int sm_count) {
     s.per = 32;
     while (s.per > 4 && N / s.per < 4LL * sm_count) s.per /= 2;
     s.list = pad256(static_cast<size_t>(N) * 4);
-    s.totals = static_cast<size_t>(s.passes) * kSortCtas * kSortBins * 4;
-    s.present = pad256(static_cast<size_t>(V));
+    s.runs = 256 + pad256(static_cast<size_t>(N / 64 + 1) * 4);
     s.part = pad256(static_cast<size_t>((N + s.per - 1) / s.per) * 2 * D * 4);
     return s;
 }
@@ -486,9 +485,9 @@ int lrscan_bwd_embed(const void *ids, int id_bytes, const void *grad_out, int gd
         a.keys[k] = reinterpret_cast<uint32_t *>(base + k * sc.list);
         a.vals[k] = reinterpret_cast<uint32_t *>(base + (2 + k) * sc.list);
     }
-    a.totals = reinterpret_cast<uint32_t *>(base + 4 * sc.list);
-    a.present = reinterpret_cast<uint8_t *>(base + 4 * sc.list + sc.totals);
-    a.part = reinterpret_cast<float *>(base + 4 * sc.list + sc.totals + sc.present);
+    a.runs = reinterpret_cast<int *>(base + 4 * sc.list);
+    a.run_at = reinterpret_cast<uint32_t *>(base + 4 * sc.list + 256);
+    a.part = reinterpret_cast<float *>(base + 4 * sc.list + sc.runs);
     a.bits = sc.bits;
     a.passes = sc.passes;
     a.per = sc.per;
