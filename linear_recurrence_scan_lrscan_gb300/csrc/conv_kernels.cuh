@@ -21,12 +21,26 @@
 
 namespace lrscan {
 
-// Bytes of each plane that a thread has in flight, and the tokens they are.
-template <class St, int V, int PLANES> struct ConvAhead {
-    static constexpr int bytes = PLANES == 1 ? 128 : 64;
-    static constexpr int per = V * static_cast<int>(sizeof(St));
-    static constexpr int tokens = bytes / per < 8 ? bytes / per : bytes / per > 16 ? 16 : bytes / per;
+// Tokens of a turn, and the turns that a thread's copies are ahead.  Wide rows
+// (V > 1) come in through shared memory: each thread copies the lanes it will
+// read itself, so that nothing waits but its own copies, and what is on its way
+// takes no registers.  Others are loaded a turn at a time.
+template <int V> struct ConvTurn {
+    static constexpr int tokens = V > 1 ? 4 : 8;
+    static constexpr int ahead = V > 1 ? 3 : 0;
 };
+template <class St, int V, int PLANES> constexpr int conv_ring_bytes() {
+    return V > 1 ? ConvTurn<V>::ahead * ConvTurn<V>::tokens * PLANES * V * static_cast<int>(sizeof(St)) * 32 * kConvSplit : 0;
+}
+template <int BYTES> __device__ __forceinline__ void conv_copy(uint32_t to, const void *from, bool in) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(in ? BYTES : 0)
+                     : "memory");
+}
+__device__ __forceinline__ void conv_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void conv_arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // The tokens t0 - (K-1) .. t0 + kConvSteps + K - 2 that start a segment, bit 0
 // the first of them; the whole warp calls it.
@@ -76,6 +90,63 @@ __device__ __forceinline__ void conv_token(const ConvArgs &a, long long b, long 
         conv_load<St, V>(static_cast<const St *>(a.x0) + (b * (K - 1) + t + (K - 1)) * a.D + d, in && a.x0 != nullptr, x);
 }
 
+// One plane's tokens on their way to a thread, turn by turn: `at` the next one
+// to be copied, `in` and `out` the places in the ring where the next turn is
+// copied to and read from.
+template <class St, int V, int PLANES> struct ConvFeed {
+    static constexpr int N = ConvTurn<V>::tokens, A = ConvTurn<V>::ahead, kBytes = V * static_cast<int>(sizeof(St));
+    static constexpr uint32_t kToken = PLANES * 32 * kConvSplit * kBytes;  // a token of all threads and planes
+    static constexpr uint32_t kRing = A * N * kToken;
+    uint32_t ring, in = 0, out = 0;
+    const St *first, *at;
+    long long stride;
+    int left;  // tokens that are there and not yet asked for
+    __device__ ConvFeed(const char *smem, int plane, const St *from, long long st, int n)
+        : ring(smem_addr(smem) + (plane * 32 * kConvSplit + threadIdx.y * 32 + threadIdx.x) * kBytes), first(from), at(from),
+          stride(st), left(n) {}
+    __device__ __forceinline__ void copy_turn() {
+        const uint32_t to = ring + in;
+        if (left >= N) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                conv_copy<kBytes>(to + j * kToken, at, true);
+                at += stride;
+            }
+        } else {
+            for (int j = 0; j < N; ++j) {
+                conv_copy<kBytes>(to + j * kToken, j < left ? at : first, j < left);
+                if (j < left) at += stride;
+            }
+        }
+        left -= N;
+        in = in + N * kToken == kRing ? 0 : in + N * kToken;
+    }
+    __device__ __forceinline__ void read_turn(typename RawOf<St, V>::T (&raw)[N]) {
+        const uint32_t from = ring + out;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if constexpr (kBytes == 16) {
+                uint4 r;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(from + j * kToken) : "memory");
+                raw[j] = make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
+            } else {
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(raw[j].x), "=r"(raw[j].y) : "r"(from + j * kToken) : "memory");
+            }
+        }
+        out = out + N * kToken == kRing ? 0 : out + N * kToken;
+    }
+    // Without a ring: the turn's tokens from memory.
+    __device__ __forceinline__ void load_turn(typename RawOf<St, V>::T (&raw)[N]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            raw[j] = conv_raw<St, V>(at, j < left);
+            at += stride;
+        }
+        left -= N;
+    }
+};
+
 // Up to N tokens from token i of the walk on; CLEAR: all taps count, and all N
 // are there.
 template <class St, int V, int K, int N, bool CLEAR>
@@ -91,7 +162,8 @@ __device__ __forceinline__ void conv_fwd_tokens(const typename RawOf<St, V>::T (
 #pragma unroll
         for (int k = 1; k < K; ++k)
             if (CLEAR || conv_counts<K>(starts, i + j, k)) vfma<V>(y, w[k], hist[k - 1], y);
-        store_lanes<St, V>(out + j * stride, y);
+        store_lanes<St, V>(out, y);
+        out += stride;
 #pragma unroll
         for (int k = K - 2; k > 0; --k)
 #pragma unroll
@@ -101,8 +173,10 @@ __device__ __forceinline__ void conv_fwd_tokens(const typename RawOf<St, V>::T (
     }
 }
 
-template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 ? 1 : 2) conv_fwd_kernel(const ConvArgs a) {
-    constexpr int N = ConvAhead<St, V, 1>::tokens;
+template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 ? 2 : 3) conv_fwd_kernel(const ConvArgs a) {
+    using Feed = ConvFeed<St, V, 1>;
+    constexpr int N = Feed::N, A = Feed::A;
+    extern __shared__ char ring[];
     const unsigned lanes = blockIdx.x % a.ndt, chunk = blockIdx.x / a.ndt;
     const long long b = blockIdx.y;
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
@@ -111,12 +185,16 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
     const uint64_t starts = conv_starts<K>(a.seg ? a.seg + b * a.T : nullptr, t0, a.T);
     if (d >= a.D) return;
     const int n = static_cast<int>(a.T - t0 < kConvSteps ? a.T - t0 : kConvSteps);
-    const St *xp = static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d;
+    Feed x(ring, 0, static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d, a.x.st, n);
     St *op = static_cast<St *>(a.o.p) + b * a.o.sb + t0 * a.o.st + d;
-    float w[K][V], bias[V], hist[K - 1][V];  // hist[k]: x_{t-1-k}; w[k]: the tap of x_{t-k}
-    typename RawOf<St, V>::T raw[N];
+    if constexpr (A > 0) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) raw[j] = conv_raw<St, V>(xp + j * a.x.st, j < n);
+        for (int turn = 0; turn < A; ++turn) {
+            x.copy_turn();
+            conv_commit();
+        }
+    }
+    float w[K][V], bias[V], hist[K - 1][V];  // hist[k]: x_{t-1-k}; w[k]: the tap of x_{t-k}
 #pragma unroll
     for (int k = K - 2; k >= 0; --k) conv_token<St, V, K>(a, b, t0 - 1 - k, d, true, hist[k]);
 #pragma unroll
@@ -125,15 +203,22 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
         for (int k = 0; k < K; ++k) w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
         bias[v] = a.bias ? __ldg(a.bias + d + v) : 0.0f;
     }
-    for (int i = 0; i < n; i += N) {
-        if (i > 0) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) raw[j] = conv_raw<St, V>(xp + (i + j) * a.x.st, i + j < n);
+    for (int turn = 0; turn * N < n; ++turn) {
+        typename RawOf<St, V>::T raw[N];
+        if constexpr (A > 0) {
+            conv_arrived<A - 1>();
+            x.read_turn(raw);
+            x.copy_turn();
+            conv_commit();
+        } else {
+            x.load_turn(raw);
         }
+        const int i = turn * N;
         if (i + N <= n && conv_clear<K>(starts, i, N))
-            conv_fwd_tokens<St, V, K, N, true>(raw, i, N, starts, w, bias, hist, op + i * a.o.st, a.o.st);
+            conv_fwd_tokens<St, V, K, N, true>(raw, i, N, starts, w, bias, hist, op, a.o.st);
         else
-            conv_fwd_tokens<St, V, K, N, false>(raw, i, n - i, starts, w, bias, hist, op + i * a.o.st, a.o.st);
+            conv_fwd_tokens<St, V, K, N, false>(raw, i, n - i, starts, w, bias, hist, op, a.o.st);
+        op += N * a.o.st;
     }
     if (a.last != nullptr && t0 + n == a.T) {
         St *to = static_cast<St *>(a.last) + b * (K - 1) * a.D + d;
@@ -194,17 +279,19 @@ __device__ __forceinline__ void conv_bwd_tokens(const ConvArgs &a, const typenam
         }
         const long long done = t - (K - 1);  // complete now
         if (CLEAR || done >= t0)
-            store_lanes<St, V>(out + (i + j - (K - 1)) * a.o.st, c.held[K - 1]);
+            store_lanes<St, V>(out, c.held[K - 1]);
         else if (done < 0 && a.grad_x0 != nullptr && done >= -(K - 1))
             store_lanes<St, V>(out0 + (done + (K - 1)) * a.D, c.held[K - 1]);
+        out += a.o.st;
     }
 }
 
 // A walk reads K - 1 tokens of grad_out past its own, for the gradients of its
 // last tokens.  The walk at token 0 holds the tokens of x0 too.
 template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 && V > 1 ? 1 : 2) conv_bwd_kernel(const ConvArgs a) {
-    constexpr int N = ConvAhead<St, V, 2>::tokens;
-    __shared__ float sums[kConvSplit][K + 1][32 * V];
+    using Feed = ConvFeed<St, V, 2>;
+    constexpr int N = Feed::N, A = Feed::A;
+    extern __shared__ char ring[];  // then the sums
     const unsigned lanes = blockIdx.x % a.ndt, chunk = blockIdx.x / a.ndt;
     const long long b = blockIdx.y;
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
@@ -220,37 +307,54 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
     if (d < a.D && t0 < a.T) {
         const int n = static_cast<int>(a.T - t0 < kConvSteps ? a.T - t0 : kConvSteps);
         const long long left = a.T - t0, tail = a.T - (K - 1);
-        const St *xp = static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d;
-        const St *gp = static_cast<const St *>(a.go.p) + b * a.go.sb + t0 * a.go.st + d;
+        const int turns = (n + K - 1 + N - 1) / N;
+        Feed x(ring, 0, static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d, a.x.st, n);
+        Feed g(ring, 1, static_cast<const St *>(a.go.p) + b * a.go.sb + t0 * a.go.st + d, a.go.st,
+               n + K - 1 < left ? n + K - 1 : static_cast<int>(left));
+        if constexpr (A > 0) {
+#pragma unroll
+            for (int turn = 0; turn < A; ++turn) {
+                x.copy_turn();
+                g.copy_turn();
+                conv_commit();
+            }
+        }
         const St *gl = static_cast<const St *>(a.grad_last) + b * (K - 1) * a.D + d;
-        St *op = static_cast<St *>(a.o.p) + b * a.o.sb + t0 * a.o.st + d;
+        St *op = static_cast<St *>(a.o.p) + b * a.o.sb + (t0 - (K - 1)) * a.o.st + d;  // of the token that is complete
         St *o0 = static_cast<St *>(a.grad_x0) + b * (K - 1) * a.D + d;
-        typename RawOf<St, V>::T xr[N], gr[N];
-        for (int i = 0; i < n + K - 1; i += N) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                xr[j] = conv_raw<St, V>(xp + (i + j) * a.x.st, i + j < n);
-                gr[j] = conv_raw<St, V>(gp + (i + j) * a.go.st, i + j < n + K - 1 && i + j < left);
+        for (int k = K - 2; k >= 0; --k) {
+            const long long t = t0 - 1 - k;
+            conv_token<St, V, K>(a, b, t, d, true, c.hist[k]);
+            // tokens before token 0 that are still among the last ones
+            conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < 0 && t >= tail, c.held[k]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int k = 0; k < K; ++k) c.w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
+        for (int turn = 0; turn < turns; ++turn) {
+            typename RawOf<St, V>::T xr[N], gr[N];
+            if constexpr (A > 0) {
+                conv_arrived<A - 1>();
+                x.read_turn(xr);
+                g.read_turn(gr);
+                x.copy_turn();
+                g.copy_turn();
+                conv_commit();
+            } else {
+                x.load_turn(xr);
+                g.load_turn(gr);
             }
-            if (i == 0) {
-#pragma unroll
-                for (int k = K - 2; k >= 0; --k) {
-                    const long long t = t0 - 1 - k;
-                    conv_token<St, V, K>(a, b, t, d, true, c.hist[k]);
-                    // tokens before token 0 that are still among the last ones
-                    conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < 0 && t >= tail, c.held[k]);
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int k = 0; k < K; ++k) c.w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
-            }
+            const int i = turn * N;
             if (i >= K - 1 && i + N <= n && conv_clear<K>(starts, i, N) && (a.grad_last == nullptr || t0 + i + N <= tail))
                 conv_bwd_tokens<St, V, K, N, true>(a, xr, gr, i, n, t0, starts, c, op, o0, gl);
             else
                 conv_bwd_tokens<St, V, K, N, false>(a, xr, gr, i, n, t0, starts, c, op, o0, gl);
+            op += N * a.o.st;
         }
     }
+    float(*sums)[K + 1][32 * V] = reinterpret_cast<float(*)[K + 1][32 * V]>(ring + conv_ring_bytes<St, V, 2>());
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll

@@ -22,6 +22,16 @@ struct PutTaps {
 
 template <class St, int V, int K> int run(const ConvArgs &a, int dir) {
     const dim3 block(32, kConvSplit);
+    constexpr int smem_f = conv_ring_bytes<St, V, 1>(), smem_b = conv_ring_bytes<St, V, 2>() + kConvSplit * (K + 1) * 32 * V * 4;
+    static bool allowed[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    if (!allowed[dev]) {
+        if (cudaFuncSetAttribute(conv_fwd_kernel<St, V, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_f) != cudaSuccess ||
+            cudaFuncSetAttribute(conv_bwd_kernel<St, V, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_b) != cudaSuccess)
+            return 1;
+        allowed[dev] = true;
+    }
     for (long long b0 = 0; b0 < a.B; b0 += 65535) {
         ConvArgs s = a;
         s.ndt = static_cast<unsigned>((a.D + 32 * V - 1) / (32 * V));
@@ -37,9 +47,9 @@ template <class St, int V, int K> int run(const ConvArgs &a, int dir) {
         if (a.part) s.part = a.part + b0 * a.chunks * (K + 1) * a.D;
         const dim3 grid(s.ndt * a.chunks, static_cast<unsigned>(s.B));
         if (dir == 0)
-            conv_fwd_kernel<St, V, K><<<grid, block, 0, a.stream>>>(s);
+            conv_fwd_kernel<St, V, K><<<grid, block, smem_f, a.stream>>>(s);
         else
-            conv_bwd_kernel<St, V, K><<<grid, block, 0, a.stream>>>(s);
+            conv_bwd_kernel<St, V, K><<<grid, block, smem_b, a.stream>>>(s);
         if (cudaGetLastError() != cudaSuccess) return 1;
     }
     return 0;
