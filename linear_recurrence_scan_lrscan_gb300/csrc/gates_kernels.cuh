@@ -265,8 +265,11 @@ template <class St, int TEAMS, int S, int PLANES, bool BULK> struct GatesGeo {
     static constexpr int kTeams = TEAMS;
     static constexpr int kWarps = TEAMS * kTeamWarps;
     static constexpr int kThreads = (kWarps + 1 + kFolds) * 32;
-    static constexpr int kPlane = kTileRows * kGatesLanes * static_cast<int>(sizeof(St));
-    static constexpr int kStage = BULK ? PLANES * kPlane : 0;
+    // Bytes of a token's lanes in a stage.  Without bulk copies they come in as
+    // 4-byte words, so that bf16 lanes may begin in the middle of one.
+    static constexpr int kPitch = kGatesLanes * static_cast<int>(sizeof(St)) + (!BULK && sizeof(St) == 2 ? 4 : 0);
+    static constexpr int kPlane = kTileRows * kPitch;
+    static constexpr int kStage = PLANES * kPlane;
     static constexpr int off_sum = S * kStage;                             // float4 [TEAMS][2][kTeamWarps][32]: a warp's map
     static constexpr int off_lam = off_sum + TEAMS * 2 * kTeamWarps * 32 * 16;  // float [TEAMS][2][kTeamWarps][64]
     static constexpr int off_in = off_lam + (PLANES == 4 ? TEAMS * 2 * kTeamWarps * 64 * 4 : 0);  // float [kSlots][64]
@@ -379,6 +382,49 @@ __device__ __forceinline__ void gates_copy_warp(const GatesArgs &g, const CUtens
     }
 }
 
+// Where rows do not fit bulk copies, each warp copies its own tokens of a tile
+// to the stage: asynchronous copies of 4-byte words, 32 a token and the 33rd of
+// a bf16 token that begins in the middle of one, all on their way at once.  A
+// word holds a lane that is there, so it may be read; tokens and words past the
+// last are zeros.
+__device__ __forceinline__ void copy_word(uint32_t to, const void *from, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(in ? 4 : 0) : "memory");
+}
+template <class St, class Geo, int PLANES>
+__device__ __forceinline__ void copy_tokens(const GatesArgs &g, const GatesTile &t, uint32_t stage, int row0, long long t0,
+                                            int left, int lane) {
+    constexpr int kSize = static_cast<int>(sizeof(St)), kWords = kGatesLanes * kSize / 4;
+    const int bytes = (g.D - t.d0 < kGatesLanes ? static_cast<int>(g.D - t.d0) : kGatesLanes) * kSize;
+    const RowsArg planes[4] = {g.r, g.i, g.x, g.go};
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p) {
+        const RowsArg &m = planes[p];
+        const uintptr_t at = reinterpret_cast<uintptr_t>(m.p) + (t.b * m.sb + t0 * m.st + t.d0) * kSize;
+        const long long step = m.st * kSize;
+        const uint32_t to = stage + p * Geo::kPlane + row0 * Geo::kPitch;
+        uintptr_t row = at;
+#pragma unroll
+        for (int l = 0; l < kTokens; ++l) {
+            const int off = static_cast<int>(row & 3);  // 0, or 2: the first word holds one lane before
+#pragma unroll
+            for (int w = 0; w < kWords; w += 32) {
+                const bool in = l < left && (lane + w) * 4 - off < bytes;
+                copy_word(to + l * Geo::kPitch + (lane + w) * 4,
+                          in ? reinterpret_cast<const void *>(row - off + (lane + w) * 4) : m.p, in);
+            }
+            row += step;
+        }
+        if constexpr (kSize == 2) {  // the 33rd words, a token a lane
+            if (lane < kTokens) {
+                const uintptr_t mine = at + lane * step;
+                const int off = static_cast<int>(mine & 3);
+                const bool in = lane < left && off != 0 && 128 - off < bytes;
+                copy_word(to + lane * Geo::kPitch + 128, in ? reinterpret_cast<const void *>(mine - off + 128) : m.p, in);
+            }
+        }
+    }
+}
+
 // The rates of this thread's two lanes, and the warp's tokens that start a
 // segment (bit l: token t0 + l).
 template <bool BULK>
@@ -461,11 +507,6 @@ __device__ __forceinline__ void gates_fold_warp(const GatesArgs &g, const float 
     }
 }
 
-// Two lanes of one token from the stage (bulk) or from memory.
-template <class St, bool BULK>
-__device__ __forceinline__ void stage_pair(const char *plane, int row, int lane, float (&x)[2]) {
-    unpack_lanes<St, 2>(reinterpret_cast<const St *>(plane) + row * kGatesLanes + 2 * lane, x);
-}
 template <class St>
 __device__ __forceinline__ float load_one(const St *p, bool in) {
     if (!in) return 0.0f;
@@ -505,17 +546,24 @@ __device__ __forceinline__ void publish_state(const GatesArgs &g, const GatesTil
     for (int v = 0; v < 2; ++v) publish1(at.state + lane_at<BULK>(lane, v), 0.0f, apply_map<SEG>(P[v], Q[v], h[v]));
 }
 
-// Two lanes of token `row` of plane p: from the stage, or from memory (t0 + l
-// the token, l < left).
-template <class St, class Geo, bool BULK, bool SLOW>
-__device__ __forceinline__ void plane_pair(const char *stage, int p, int row, const RowsArg &m, long long at, int l,
-                                           const bool (&in)[2], int left, int lane, float (&x)[2]) {
+// Two lanes of token `row` of the stage, token l of the warp; `at`: where the
+// warp's first token is in the plane's memory.
+template <class St, class Geo, bool BULK>
+__device__ __forceinline__ void plane_pair(const char *stage, int p, int row, const RowsArg &m, long long at, int l, int lane,
+                                           float (&x)[2]) {
+    const char *plane = stage + p * Geo::kPlane + row * Geo::kPitch;
     if constexpr (BULK) {
-        stage_pair<St, BULK>(stage + p * Geo::kPlane, row, lane, x);
+        unpack_lanes<St, 2>(reinterpret_cast<const St *>(plane) + 2 * lane, x);
     } else {
+        // the token's first lane may be the second of its first word
+        const int off = sizeof(St) == 2 ? (static_cast<int>(reinterpret_cast<uintptr_t>(m.p) >> 1) + static_cast<int>(at) +
+                                           l * static_cast<int>(m.st)) & 1 : 0;
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-            x[v] = load_one(static_cast<const St *>(m.p) + at + l * m.st + lane_at<BULK>(lane, v), !SLOW || (in[v] && l < left));
+        for (int v = 0; v < 2; ++v) {
+            float y[1];
+            unpack_lanes<St, 1>(reinterpret_cast<const St *>(plane) + off + lane_at<BULK>(lane, v), y);
+            x[v] = y[0];
+        }
     }
 }
 
@@ -533,9 +581,9 @@ __device__ __forceinline__ void gates_fwd_tokens(const GatesArgs &g, const char 
 #pragma unroll
     for (int l = 0; l < L; ++l) {
         float r[2], i[2], x[2], rg[2], ig[2], G[2], sq[2], rs[2];
-        plane_pair<St, Geo, BULK, SLOW>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
-        plane_pair<St, Geo, BULK, SLOW>(stage, 1, row0 + l, g.i, ai, l, in, left, lane, i);
-        plane_pair<St, Geo, BULK, SLOW>(stage, 2, row0 + l, g.x, ax, l, in, left, lane, x);
+        plane_pair<St, Geo, BULK>(stage, 0, row0 + l, g.r, ar, l, lane, r);
+        plane_pair<St, Geo, BULK>(stage, 1, row0 + l, g.i, ai, l, lane, i);
+        plane_pair<St, Geo, BULK>(stage, 2, row0 + l, g.x, ax, l, lane, x);
         sigmoid2(rg, r);
         sigmoid2(ig, i);
         decay2<SLOW>(k, rg, G, a[l], sq, rs);
@@ -627,8 +675,11 @@ gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
         if (t.n >= 0) {  // on their way while the planes come in
             tile_rates<BULK>(g, t, lane, in, k);
             if constexpr (SEG) seg = first_token(g, t, t0, left, lane);
+            if constexpr (!BULK)
+                copy_tokens<St, Geo, 3>(g, t, smem_addr(smem) + s * Geo::kStage, warp * L, t0, left, lane);
         }
         ok = ok && mbar_wait(bars.full + 8 * s, (it / S) & 1, wc, kSiteConsumerFull);
+        if constexpr (!BULK) asm volatile("cp.async.wait_all;" ::: "memory");
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) t.n = -1;
         float a[L][2], b[L][2], P[2], Q[2];
@@ -712,8 +763,8 @@ __device__ __forceinline__ void gates_bwd_decays(const GatesArgs &g, const char 
 #pragma unroll
     for (int l = kTokens - 1; l >= 0; --l) {
         float r[2], go[2], rg[2], G[2], m[2];
-        plane_pair<St, Geo, BULK, SLOW>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
-        plane_pair<St, Geo, BULK, SLOW>(stage, 3, row0 + l, g.go, ag, l, in, left, lane, go);
+        plane_pair<St, Geo, BULK>(stage, 0, row0 + l, g.r, ar, l, lane, r);
+        plane_pair<St, Geo, BULK>(stage, 3, row0 + l, g.go, ag, l, lane, go);
         sigmoid2(rg, r);
         decay_only2<SLOW>(k, rg, G, a[l], m);
         if (SLOW && l >= left) a[l][0] = a[l][1] = 1.0f;
@@ -738,7 +789,7 @@ __device__ __forceinline__ void gates_bwd_adjoints(const GatesArgs &g, const cha
 #pragma unroll
     for (int l = kTokens - 1; l >= 0; --l) {
         float go[2];
-        plane_pair<St, Geo, BULK, SLOW>(stage, 3, row0 + l, g.go, ag, l, in, left, lane, go);
+        plane_pair<St, Geo, BULK>(stage, 3, row0 + l, g.go, ag, l, lane, go);
         add_x2(go[0], go[1], go[0], go[1], cc[0], cc[1]);
         if (SEG && ((first >> l) & 1u))
             cc[0] = cc[1] = 0.0f;
@@ -765,9 +816,9 @@ __device__ __forceinline__ void gates_bwd_grads(const GatesArgs &g, const char *
     for (int l = 0; l < kTokens; ++l) {
         if (SLOW && l >= left) break;
         float r[2], i[2], x[2], rg[2], ig[2], G[2], a[2], sq[2], rs[2], ix[2], q[2], yr[2], yi[2], yx[2], w[2], z[2];
-        plane_pair<St, Geo, BULK, SLOW>(stage, 0, row0 + l, g.r, ar, l, in, left, lane, r);
-        plane_pair<St, Geo, BULK, SLOW>(stage, 1, row0 + l, g.i, ai, l, in, left, lane, i);
-        plane_pair<St, Geo, BULK, SLOW>(stage, 2, row0 + l, g.x, ax, l, in, left, lane, x);
+        plane_pair<St, Geo, BULK>(stage, 0, row0 + l, g.r, ar, l, lane, r);
+        plane_pair<St, Geo, BULK>(stage, 1, row0 + l, g.i, ai, l, lane, i);
+        plane_pair<St, Geo, BULK>(stage, 2, row0 + l, g.x, ax, l, lane, x);
         sigmoid2(rg, r);
         sigmoid2(ig, i);
         decay2<SLOW>(k, rg, G, a, sq, rs);
@@ -860,8 +911,11 @@ gates_bwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
             for (int v = 0; v < 2; ++v)
                 if (in[v] && left > 0)
                     h[v] = __ldg(g.saved + (t.b * ns + t0 / kGatesSave) * g.D + t.d0 + lane_at<BULK>(lane, v));
+            if constexpr (!BULK)
+                copy_tokens<St, Geo, 4>(g, t, smem_addr(smem) + s * Geo::kStage, warp * L, t0, left, lane);
         }
         ok = ok && mbar_wait(bars.full + 8 * s, (it / S) & 1, wc, kSiteConsumerFull);
+        if constexpr (!BULK) asm volatile("cp.async.wait_all;" ::: "memory");
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) t.n = -1;
         float a[L][2], P[2], Q[2];
