@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float *part, lo
     const long long r0 = per * blockIdx.y, r1 = r0 + per < rows ? r0 + per : rows;
     float sum = 0.0f;
     pdl_wait();
+    pdl_trigger();
     if (d < cols) {
 #pragma unroll 8
         for (long long r = r0 + warp; r < r1; r += 32) sum += __ldg(part + r * cols + d);

@@ -296,6 +296,7 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
     const long long b = blockIdx.y;
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
     const long long t0 = (static_cast<long long>(chunk) * kConvSplit + threadIdx.y) * kConvSteps;
+    pdl_trigger();  // the reduction waits for this grid's end all the same
     ConvWalk<V, K> c;
 #pragma unroll
     for (int v = 0; v < V; ++v) {

@@ -107,6 +107,8 @@ __device__ __forceinline__ void decay2(const float (&k)[2], const float (&rg)[2]
 __global__ void __launch_bounds__(256) gates_begin_kernel(uint4 *words, long long n, const float *lam, float c, long long D,
                                                           float *rate) {
     const long long first = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, step = 256LL * gridDim.x;
+    pdl_wait();
+    pdl_trigger();
     for (long long j = first; j < n; j += step) words[j] = make_uint4(~0u, ~0u, ~0u, ~0u);
     for (long long d = first; d < D; d += step) rate[d] = gate_rate(__ldg(lam + d), c);
 }
@@ -257,7 +259,6 @@ static_assert(kTileRows == kGatesTileRows, "the host counts tiles alike");
 constexpr int kFolds = 3;
 constexpr int kSlots = 8;                          // of entering states
 constexpr int kRing = 16;                          // of tiles' names
-constexpr int kAhead = 1;                          // tiles named before a team is free for them
 
 // TEAMS teams, then the copy warp and the fold warps; S stages, TEAMS at least.
 template <class St, int TEAMS, int S, int PLANES, bool BULK> struct GatesGeo {
@@ -325,8 +326,7 @@ __device__ __forceinline__ bool tile_of(const GatesArgs &g, unsigned tk, GatesTi
 }
 
 // The copy warp, both directions (one thread of it): takes tickets, names the
-// tiles and copies their planes in.  The next ticket is asked for while the
-// stage is not yet free.
+// tiles and copies their planes in.
 template <class Geo, bool BULK, bool BWD, int PLANES, int S>
 __device__ __forceinline__ void gates_copy_warp(const GatesArgs &g, const CUtensorMap *const (&maps)[4], char *smem,
                                                 const GatesBars<Geo, S> &bars, const WaitCtx &wc) {
@@ -336,22 +336,26 @@ __device__ __forceinline__ void gates_copy_warp(const GatesArgs &g, const CUtens
     auto ticket = [&](unsigned last) -> unsigned {
         return one ? last + gridDim.x : atomicAdd(g.ticket, 1u) + 1u;  // the word starts as all ones
     };
-    unsigned tk = one ? blockIdx.x : ticket(0);
+    // A ticket taken before a team is free for its tile holds up the tiles that
+    // follow it in other CTAs.  So where the lane tiles are fewer than the CTAs,
+    // and tiles in flight follow one another, it is taken as a team comes to its
+    // last walk (65536 tokens of 2560 fp32 lanes with restarts: 493 us forward,
+    // 607 two tiles earlier); else two tiles earlier, so that the copies are in
+    // when the team comes (8 x 2048 x 2560 bf16: 72 us forward, 78 later).
+    const int ahead = g.nl >= static_cast<int>(gridDim.x) ? 2 : 0;
+    unsigned tk = blockIdx.x - gridDim.x;
     int issued = 0, ends = 0;
     bool ok = true;
     for (int it = 0;; ++it) {
         const int s = it % S;
         GatesTile t;
-        const bool end = !tile_of(g, tk, t);
-        unsigned next = tk;
-        if (!end) next = ticket(tk);
         ok = *wc.abort_flag == 0 && mbar_wait(bars.empty + 8 * s, ((it / S) & 1) ^ 1, wc, kSiteProducerEmpty);
-        // a ticket taken long before a team is free holds up the tiles that
-        // follow it in other CTAs
-        const int before = it - Geo::kTeams - kAhead;
-        if (ok && before >= 0 && !end)
+        const int before = it - Geo::kTeams - ahead;
+        if (ok && before >= 0 && ends == 0)
             ok = mbar_wait(bars.hempty + 8 * (before % kSlots), (before / kSlots) & 1, wc, kSiteProducerEmpty);
         if (!ok) break;
+        if (ends == 0) tk = ticket(tk);
+        const bool end = !tile_of(g, tk, t);
         tile[it % kRing] = t;
         mbar_arrive(bars.named + 8 * (it % kRing));
         if (BULK && !end) {
@@ -367,7 +371,6 @@ __device__ __forceinline__ void gates_copy_warp(const GatesArgs &g, const CUtens
         }
         // every team and fold warp sees an end of its own
         if (end && ++ends == (Geo::kTeams > kFolds ? Geo::kTeams : kFolds)) break;
-        tk = next;
     }
     if (BULK && !ok) {
         // leaving early: no copy of this CTA may still be on its way
@@ -647,6 +650,8 @@ gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
         bars.init();
     }
     __syncthreads();
+    pdl_wait();
+    pdl_trigger();
     if (threadIdx.x / 32 == Geo::kWarps) {
         const CUtensorMap *const maps[4] = {&mr, &mi, &mx, nullptr};
         gates_copy_warp<Geo, BULK, false, 3, S>(g, maps, smem, bars, wc);
@@ -875,6 +880,8 @@ gates_bwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
         bars.init();
     }
     __syncthreads();
+    pdl_wait();
+    pdl_trigger();
     if (threadIdx.x / 32 == Geo::kWarps) {
         const CUtensorMap *const maps[4] = {&mr, &mi, &mx, &mg};
         gates_copy_warp<Geo, BULK, true, 4, S>(g, maps, smem, bars, wc);

@@ -41,9 +41,8 @@ template <class St, bool BULK, bool SEG> int fwd(const GatesLaunch &L, int sm_co
     const int fit = resident(kern, Geo::kThreads, Geo::kBytes, cache, &dev);
     if (fit == 0) return 1;
     const long long tiles = static_cast<long long>(L.a.nl) * L.a.nc, most = static_cast<long long>(fit) * sm_count;
-    kern<<<static_cast<unsigned>(tiles < most ? tiles : most), Geo::kThreads, Geo::kBytes, L.stream>>>(
-        L.a, L.maps[0], L.maps[1], L.maps[2]);
-    return cudaGetLastError() != cudaSuccess;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(Geo::kThreads), Geo::kBytes,
+                      L.stream, L.a, L.maps[0], L.maps[1], L.maps[2]) != cudaSuccess;
 }
 
 template <class St, bool BULK, bool SEG> int bwd(const GatesLaunch &L, int sm_count) {
@@ -55,9 +54,8 @@ template <class St, bool BULK, bool SEG> int bwd(const GatesLaunch &L, int sm_co
     const int fit = resident(kern, Geo::kThreads, Geo::kBytes, cache, &dev);
     if (fit == 0) return 1;
     const long long tiles = static_cast<long long>(L.a.nl) * L.a.nc, most = static_cast<long long>(fit) * sm_count;
-    kern<<<static_cast<unsigned>(tiles < most ? tiles : most), Geo::kThreads, Geo::kBytes, L.stream>>>(
-        L.a, L.maps[0], L.maps[1], L.maps[2], L.maps[3]);
-    return cudaGetLastError() != cudaSuccess;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(Geo::kThreads), Geo::kBytes,
+                      L.stream, L.a, L.maps[0], L.maps[1], L.maps[2], L.maps[3]) != cudaSuccess;
 }
 
 template <class St> int pick(const GatesLaunch &L, int dir, int sm_count) {
@@ -123,9 +121,8 @@ int gates_begin_launch(void *words, size_t bytes, const float *lam, float c, lon
                        cudaStream_t stream) {
     const long long n = static_cast<long long>(bytes / 16), most = n > D ? n : D;
     const long long blocks = (most + 255) / 256;
-    gates_begin_kernel<<<static_cast<unsigned>(blocks < 4LL * sm_count ? blocks : 4LL * sm_count), 256, 0, stream>>>(
-        static_cast<uint4 *>(words), n, lam, c, D, rate);
-    return cudaGetLastError() != cudaSuccess;
+    return launch_pdl(gates_begin_kernel, dim3(static_cast<unsigned>(blocks < 4LL * sm_count ? blocks : 4LL * sm_count)),
+                      dim3(256), 0, stream, static_cast<uint4 *>(words), n, lam, c, D, rate) != cudaSuccess;
 }
 
 int gates_finish_slices(long long rows) { return column_slices(rows); }
