@@ -28,6 +28,7 @@ struct EmbedArgs {
     int bits;                     // of a digit
     int passes;
     int per;                      // sorted tokens of a stretch
+    int zeros;                    // CTAs of the second kernel that write zeros
     int held;                     // tokens of a CTA that the sort keeps on chip, or 0
 };
 
@@ -35,6 +36,7 @@ constexpr int kSortCtas = 8;      // one cluster
 constexpr int kSortWarps = 32;
 constexpr int kSortBits = 9;      // most bits of a digit
 constexpr int kSortBins = 1 << kSortBits;
+constexpr int kLongRun = 32;      // a run of more tokens than this is shared
 
 int embed_fwd_launch(const EmbedArgs &a, int wdtype, int odtype);
 int embed_bwd_launch(const EmbedArgs &a, int gdtype, int wdtype);

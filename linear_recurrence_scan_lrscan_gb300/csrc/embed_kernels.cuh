@@ -3,14 +3,15 @@
 // with ids[n] = v, in the order of the tokens (two calls agree bit for bit).
 // A negative id is no token: a row of zeros, and no gradient.
 //
-// Backward in three kernels.  In the first, one cluster sorts the tokens by id,
-// stably, by digits of up to 9 bits: each warp counts the digits of its own
-// stretch of tokens, the counts become every warp's first places, and the warp
-// moves its tokens there.  Meanwhile the other CTAs write the zeros of the rows
-// that have no token, most of what is written for a large table; each finds its
-// rows' tokens by reading all ids once.  In the second, CTAs sum the rows of
-// equal stretches of the sorted tokens.  A run of one id is summed by the CTA it
-// starts in, up to 64 tokens past its stretch; a longer run takes every CTA it
+// Backward in three kernels.  The first sorts the tokens by id, stably, by digits
+// of up to 9 bits, on one cluster: each warp counts the digits of its own stretch
+// of tokens, the counts become every warp's first places, and the warp moves its
+// tokens there.  The second begins beside it: one CTA an SM writes the zeros of
+// the rows that have no token, most of what is written for a large table, and
+// finds its rows' tokens by reading all ids once.  The others wait for the sort
+// and sum the rows of equal stretches of the sorted tokens; while they wait for
+// rows, the zeros keep the memory busy.  A run of one id is summed by the CTA it
+// starts in, up to 32 tokens past its stretch; a longer run takes every CTA it
 // touches, which leave fp32 sums, and the third kernel adds those up.
 #pragma once
 
@@ -101,8 +102,8 @@ __device__ __forceinline__ unsigned same_digit(unsigned digit, int bits) {
 }
 
 constexpr int kSortAhead = 8;        // tokens of a lane in flight
-constexpr int kZeroSpan = 32768;     // rows whose tokens a zeroing CTA looks for at once
-constexpr int kZeroBytes = 4096;     // most bytes of a bulk copy of zeros
+constexpr int kZeroSpan = 8192;      // rows whose tokens a zeroing CTA looks for at once
+constexpr int kZeroBytes = 16384;    // most bytes of a bulk copy of zeros
 
 // Bulk copy shared -> global: both on 16-byte boundaries, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_store(void *to, const void *from, uint32_t bytes) {
@@ -110,71 +111,17 @@ __device__ __forceinline__ void bulk_store(void *to, const void *from, uint32_t 
                  : "memory");
 }
 
-// The rows v0 .. v1-1 of the table that no token has: zeros.  Rows on 16-byte
-// boundaries (V > 1) leave as bulk copies of a block of zeros.
-template <class O, int V>
-__device__ __forceinline__ void embed_zero_rows(const EmbedArgs &a, long long v0, long long v1, uint32_t *bits) {
-    __shared__ alignas(16) uint4 zeros[V > 1 ? kZeroBytes / 16 : 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if constexpr (V > 1) {
-        for (int j = threadIdx.x; j < kZeroBytes / 16; j += blockDim.x) zeros[j] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-    }
-    for (long long first = v0; first < v1; first += kZeroSpan) {
-        const int span = static_cast<int>(v1 - first < kZeroSpan ? v1 - first : kZeroSpan);
-        for (int j = threadIdx.x; j < (span + 31) / 32; j += blockDim.x) bits[j] = 0;
-        __syncthreads();
-        for (long long n0 = threadIdx.x; n0 < a.N; n0 += kSortAhead * blockDim.x) {
-            long long id[kSortAhead];
-#pragma unroll
-            for (int k = 0; k < kSortAhead; ++k) {
-                const long long n = n0 + static_cast<long long>(k) * blockDim.x;
-                id[k] = n < a.N ? token_id(a, n) - first : -1;
-            }
-#pragma unroll
-            for (int k = 0; k < kSortAhead; ++k)
-                if (id[k] >= 0 && id[k] < span) atomicOr(bits + id[k] / 32, 1u << (id[k] % 32));
-        }
-        __syncthreads();
-        for (int r = warp; r < span; r += warps) {
-            if (bits[r / 32] >> (r % 32) & 1u) continue;
-            O *row = static_cast<O *>(a.out) + (first + r) * a.D;
-            if constexpr (V > 1) {
-                const long long bytes = a.D * static_cast<long long>(sizeof(O));
-                if (lane == 0)
-                    for (long long at = 0; at < bytes; at += kZeroBytes)
-                        bulk_store(reinterpret_cast<char *>(row) + at, zeros,
-                                   static_cast<uint32_t>(bytes - at < kZeroBytes ? bytes - at : kZeroBytes));
-            } else {
-                const float zero[1] = {0.0f};
-                for (long long d = lane; d < a.D; d += 32) store_lanes<O, 1>(row + d, zero);
-            }
-        }
-        __syncthreads();
-    }
-    if constexpr (V > 1) {
-        bulk_commit();
-        bulk_wait<0>();
-    }
-}
-
-// The first cluster sorts (id, token number) by id, stably; the others write
-// zeros.  While the zeros take the memory's bandwidth a round trip to it is slow,
-// so the tokens between two passes stay in the cluster's shared memory where
-// they fit (`a.held` tokens a CTA; 0: in memory).
-template <class O, int V>
+// The cluster sorts (id, token number) by id, stably.  While the zeros take the
+// memory's bandwidth a round trip to it is slow, so the tokens between two passes
+// stay in the cluster's shared memory where they fit (`a.held` tokens a CTA; 0: in
+// memory).
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortWarps * 32, 1)
 embed_sort_kernel(const EmbedArgs a) {
     extern __shared__ uint32_t count[];  // [kSortWarps][bins + 1]: a warp's counts, then its next places;
                                          // then the tokens held: [2] x [key, val] x [a.held]
     __shared__ uint32_t base[kSortBins], totals[kSortBins];
     __shared__ uint32_t sums[kSortBins / 32];
-    if (blockIdx.x >= kSortCtas) {
-        const long long ctas = gridDim.x - kSortCtas, me = blockIdx.x - kSortCtas;
-        const long long each = (a.V + ctas - 1) / ctas, v0 = me * each;
-        embed_zero_rows<O, V>(a, v0 < a.V ? v0 : a.V, v0 + each < a.V ? v0 + each : a.V, count);
-        return;
-    }
+    pdl_trigger();
     const int bins = 1 << a.bits, row = bins + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned rank = blockIdx.x;
@@ -309,18 +256,75 @@ __device__ __forceinline__ void put_row(const EmbedArgs &a, long long id, long l
 
 constexpr int kSumAhead = 8;     // rows in flight a thread
 constexpr int kMostPer = 32;     // most sorted tokens of a stretch
-constexpr int kLongRun = 64;     // a run of more tokens than this is shared
 
-template <class G, class O, int V> __global__ void __launch_bounds__(512) embed_sum_kernel(const EmbedArgs a) {
+// The rows v0 .. v1-1 of the table that no token has: zeros.  Rows on 16-byte
+// boundaries (V > 1) leave as bulk copies of a block of zeros.
+template <class O, int V>
+__device__ __forceinline__ void embed_zero_rows(const EmbedArgs &a, long long v0, long long v1) {
+    __shared__ uint32_t bits[kZeroSpan / 32];
+    __shared__ alignas(16) uint4 zeros[V > 1 ? kZeroBytes / 16 : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if constexpr (V > 1) {
+        for (int j = threadIdx.x; j < kZeroBytes / 16; j += blockDim.x) zeros[j] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    for (long long first = v0; first < v1; first += kZeroSpan) {
+        const int span = static_cast<int>(v1 - first < kZeroSpan ? v1 - first : kZeroSpan);
+        for (int j = threadIdx.x; j < (span + 31) / 32; j += blockDim.x) bits[j] = 0;
+        __syncthreads();
+        for (long long n0 = threadIdx.x; n0 < a.N; n0 += kSortAhead * blockDim.x) {
+            long long id[kSortAhead];
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k) {
+                const long long n = n0 + static_cast<long long>(k) * blockDim.x;
+                id[k] = n < a.N ? token_id(a, n) - first : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kSortAhead; ++k)
+                if (id[k] >= 0 && id[k] < span) atomicOr(bits + id[k] / 32, 1u << (id[k] % 32));
+        }
+        __syncthreads();
+        for (int r = warp; r < span; r += warps) {
+            if (bits[r / 32] >> (r % 32) & 1u) continue;
+            O *row = static_cast<O *>(a.out) + (first + r) * a.D;
+            if constexpr (V > 1) {
+                const long long bytes = a.D * static_cast<long long>(sizeof(O));
+                if (lane == 0)
+                    for (long long at = 0; at < bytes; at += kZeroBytes)
+                        bulk_store(reinterpret_cast<char *>(row) + at, zeros,
+                                   static_cast<uint32_t>(bytes - at < kZeroBytes ? bytes - at : kZeroBytes));
+            } else {
+                const float zero[1] = {0.0f};
+                for (long long d = lane; d < a.D; d += 32) store_lanes<O, 1>(row + d, zero);
+            }
+        }
+        __syncthreads();
+    }
+    if constexpr (V > 1) {
+        bulk_commit();
+        bulk_wait<0>();
+    }
+}
+
+// U groups of V lanes a thread, a block's width apart.  The first a.zeros CTAs
+// write zeros.
+template <class G, class O, int V, int U> __global__ void __launch_bounds__(512) embed_sum_kernel(const EmbedArgs a) {
     // the sorted tokens from kLongRun before the stretch to kLongRun after it
     __shared__ uint32_t key[kMostPer + 2 * kLongRun + 1], val[kMostPer + kLongRun];
     __shared__ int from, to;
+    const long long block = static_cast<long long>(blockIdx.x) - a.zeros;
+    if (block < 0) {
+        const long long each = (a.V + a.zeros - 1) / a.zeros, v0 = blockIdx.x * each;
+        if (blockIdx.y == 0) embed_zero_rows<O, V>(a, v0 < a.V ? v0 : a.V, v0 + each < a.V ? v0 + each : a.V);
+        return;
+    }
     pdl_wait();
     const uint32_t *keys = a.passes & 1 ? a.keys[1] : a.keys[0], *vals = a.passes & 1 ? a.vals[1] : a.vals[0];
     const uint32_t none = static_cast<uint32_t>(a.V);
-    const long long j0 = static_cast<long long>(blockIdx.x) * a.per;
+    const long long j0 = block * a.per;
     const int n = static_cast<int>(a.N - j0 < a.per ? a.N - j0 : a.per);
-    const long long d = (static_cast<long long>(blockIdx.y) * blockDim.x + threadIdx.x) * V;
+    const long long d = (static_cast<long long>(blockIdx.y) * U * blockDim.x + threadIdx.x) * V;
+    const int apart = blockDim.x * V;
     for (int j = threadIdx.x; j < n + 2 * kLongRun + 1; j += blockDim.x) {
         const long long at = j0 + j - kLongRun;
         key[j] = at >= 0 && at < a.N ? keys[at] : none;
@@ -368,48 +372,62 @@ template <class G, class O, int V> __global__ void __launch_bounds__(512) embed_
     if (d >= a.D) return;
     const G *rows = static_cast<const G *>(a.in) + d;
     const int last = to;
-    float sum[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+    const long long left = (a.D - d + apart - 1) / apart;
+    const int groups = left < U ? static_cast<int>(left) : U;
+    float sum[U][V] = {};
     bool opened = mid[from] != mid[from - 1];  // the current id's run starts here
     for (int i0 = from; i0 < last; i0 += kSumAhead) {
-        typename RawOf<G, V>::T raw[kSumAhead];
+        typename RawOf<G, V>::T raw[kSumAhead][U];
 #pragma unroll
         for (int i = 0; i < kSumAhead; ++i)
-            if (i0 + i < last && mid[i0 + i] != none) raw[i] = load_raw<G, V>(rows + static_cast<long long>(val[i0 + i]) * a.D);
+            if (i0 + i < last && mid[i0 + i] != none) {
+                const G *row = rows + static_cast<long long>(val[i0 + i]) * a.D;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < groups) raw[i][u] = load_raw<G, V>(row + u * apart);
+            }
 #pragma unroll
         for (int i = 0; i < kSumAhead; ++i) {
             if (i0 + i >= last) break;
             const uint32_t id = mid[i0 + i];
             if (id == none) return;  // the tokens that are none come last
-            float x[V];
-            widen_raw(raw[i], x);
 #pragma unroll
-            for (int v = 0; v < V; ++v) sum[v] += x[v];
+            for (int u = 0; u < U; ++u) {
+                float x[V];
+                widen_raw(raw[i][u], x);
+#pragma unroll
+                for (int v = 0; v < V; ++v) sum[u][v] += x[v];
+            }
             const bool ends = mid[i0 + i + 1] != id;
             if (!ends && i0 + i + 1 < last) continue;
-            if (ends && opened) {
-                put_row<O, V>(a, id, d, sum);
-            } else {  // a long run's share: it came in (slot 0) or starts here (slot 1)
-                float *at = a.part + (static_cast<long long>(blockIdx.x) * 2 + (opened ? 1 : 0)) * a.D + d;
+            // a long run's share: it came in (slot 0) or starts here (slot 1)
+            float *share = a.part + (block * 2 + (opened ? 1 : 0)) * a.D + d;
 #pragma unroll
-                for (int v = 0; v < V; ++v) at[v] = sum[v];
+            for (int u = 0; u < U; ++u) {
+                if (u < groups) {
+                    if (ends && opened) {
+                        put_row<O, V>(a, id, d + u * apart, sum[u]);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) share[u * apart + v] = sum[u][v];
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) sum[u][v] = 0.0f;
             }
             opened = true;
-#pragma unroll
-            for (int v = 0; v < V; ++v) sum[v] = 0.0f;
         }
     }
 }
 
-// The long runs, 32 columns a turn: the eight warps take every eighth stretch,
+// The long runs, 32 V columns a turn: the eight warps take every eighth stretch,
 // and their sums are added in warp order.
-template <class O> __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedArgs a) {
-    __shared__ float sums[8][33];
+template <class O, int V> __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedArgs a) {
+    __shared__ float sums[8][V][33];
     pdl_wait();
     const uint32_t *keys = a.passes & 1 ? a.keys[1] : a.keys[0];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long columns = (a.D + 31) / 32, turns = static_cast<long long>(*a.runs) * columns;
+    const long long columns = (a.D + 32 * V - 1) / (32 * V), turns = static_cast<long long>(*a.runs) * columns;
     for (long long turn = blockIdx.x; turn < turns; turn += gridDim.x) {
         const long long at = a.run_at[turn / columns], first = at / a.per;
         const uint32_t id = keys[at];
@@ -421,20 +439,30 @@ template <class O> __global__ void __launch_bounds__(256) embed_join_kernel(cons
             more = __syncthreads_count(j < stretches && keys[j * a.per] == id);
             lo += more;
         }
-        const long long d = turn % columns * 32 + lane;
-        float sum = 0.0f;
+        const long long d = (turn % columns * 32 + lane) * V;
+        float sum[V] = {};
         if (d < a.D) {
-            if (warp == 0) sum = a.part[(first * 2 + 1) * a.D + d];
+            auto share = [&](long long slot) {
+                float x[V];
+                unpack_lanes<float, V>(a.part + slot * a.D + d, x);
+#pragma unroll
+                for (int v = 0; v < V; ++v) sum[v] += x[v];
+            };
+            if (warp == 0) share(first * 2 + 1);
 #pragma unroll 8
-            for (long long j = first + 1 + warp; j <= lo; j += 8) sum += a.part[j * 2 * a.D + d];
+            for (long long j = first + 1 + warp; j <= lo; j += 8) share(j * 2);
         }
-        sums[warp][lane] = sum;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sums[warp][v][lane] = sum[v];
         __syncthreads();
         if (warp == 0 && d < a.D) {
-            float x[1] = {0.0f};
 #pragma unroll
-            for (int w = 0; w < 8; ++w) x[0] += sums[w][lane];
-            put_row<O, 1>(a, id, d, x);
+            for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+#pragma unroll
+                for (int v = 0; v < V; ++v) sum[v] += sums[w][v][lane];
+            put_row<O, V>(a, id, d, sum);
         }
         __syncthreads();
     }

@@ -26,28 +26,6 @@ template <class W, class O, int V> int fwd(const EmbedArgs &a) {
 
 template <class G, class O, int V> int bwd_vec(EmbedArgs a) {
     constexpr int kMost = 212 * 1024;  // beside 8 KB that are static
-    static int fit[64] = {};  // clusters that run at once: fewer than SMs / 8, as a cluster stays within its part of the GPU
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    if (fit[dev] == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kSortCtas);
-        cfg.blockDim = dim3(kSortWarps * 32);
-        cfg.dynamicSmemBytes = kMost;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = kSortCtas;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaFuncSetAttribute(embed_sort_kernel<O, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, embed_sort_kernel<O, V>, &cfg) != cudaSuccess)
-            return 1;
-        fit[dev] = n > 1 ? n : 2;
-    }
-    // one cluster sorts, the others write zeros
-    const int clusters = a.add ? 1 : fit[dev];
     int smem = kSortWarps * ((1 << a.bits) + 1) * 4;
     const long long stretch = ((a.N + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
     const long long held = stretch * kSortWarps;  // tokens of a CTA
@@ -56,18 +34,21 @@ template <class G, class O, int V> int bwd_vec(EmbedArgs a) {
         a.held = static_cast<int>(held);
         smem += static_cast<int>(held * 16);
     }
-    embed_sort_kernel<O, V><<<clusters * kSortCtas, kSortWarps * 32, smem, a.stream>>>(a);
+    if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) return 1;
+    embed_sort_kernel<<<kSortCtas, kSortWarps * 32, smem, a.stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return 1;
     const long long lanes = (a.D + V - 1) / V;
-    const long long ny = (lanes + 511) / 512;  // a row's lanes in equal parts
-    const int threads = static_cast<int>(((lanes + ny - 1) / ny + 31) / 32 * 32);
-    const long long blocks = (a.N + a.per - 1) / a.per;
+    constexpr int U = V == 1 ? 4 : 1;
+    const long long ny = (lanes + 512 * U - 1) / (512 * U);  // a row's lanes in equal parts
+    const int threads = static_cast<int>(((lanes + U * ny - 1) / (U * ny) + 31) / 32 * 32);
+    a.zeros = a.add ? 0 : 2 * a.sm_count;
+    const long long blocks = a.zeros + (a.N + a.per - 1) / a.per;
     if (blocks > 0x7fffffffLL || ny > 65535) return 1;
-    if (launch_pdl(embed_sum_kernel<G, O, V>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(ny)), dim3(threads), 0,
+    if (launch_pdl(embed_sum_kernel<G, O, V, U>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(ny)), dim3(threads), 0,
                    a.stream, a) != cudaSuccess)
         return 1;
     if (a.N <= kLongRun) return 0;
-    return launch_pdl(embed_join_kernel<O>, dim3(8 * a.sm_count), dim3(256), 0, a.stream, a) != cudaSuccess;
+    return launch_pdl(embed_join_kernel<O, (V > 1 ? 4 : 1)>, dim3(8 * a.sm_count), dim3(256), 0, a.stream, a) != cudaSuccess;
 }
 
 template <class G, class O> int bwd(const EmbedArgs &a) { return a.vec ? bwd_vec<G, O, kWide<G, O>>(a) : bwd_vec<G, O, 1>(a); }

@@ -223,11 +223,11 @@ EmbedScratch embed_scratch(int64_t N, int64_t V, int64_t D, int sm_count) {
     s.passes = (bits + kSortBits - 1) / kSortBits;
     s.bits = (bits + s.passes - 1) / s.passes;
     if (s.bits < 5) s.bits = 5;
-    // stretches short enough for four CTAs a SM, and long enough that few sums are left in between
+    // stretches short enough for two CTAs an SM, and long enough that few sums are left in between
     s.per = 32;
-    while (s.per > 4 && N / s.per < 4LL * sm_count) s.per /= 2;
+    while (s.per > 4 && N / s.per < 2LL * sm_count) s.per /= 2;
     s.list = pad256(static_cast<size_t>(N) * 4);
-    s.runs = 256 + pad256(static_cast<size_t>(N / 64 + 1) * 4);
+    s.runs = 256 + pad256(static_cast<size_t>(N / kLongRun + 1) * 4);
     s.part = pad256(static_cast<size_t>((N + s.per - 1) / s.per) * 2 * D * 4);
     return s;
 }
