@@ -24,13 +24,15 @@ namespace lrscan {
 // Tokens of a turn, and the turns that a thread's copies are ahead.  Wide rows
 // (V > 1) come in through shared memory: each thread copies the lanes it will
 // read itself, so that nothing waits but its own copies, and what is on its way
-// takes no registers.  Others are loaded a turn at a time.
-template <int V> struct ConvTurn {
+// takes no registers.  Others are loaded a turn at a time.  Forward 8 x 2048 x
+// 2560 bf16: 33 us four turns ahead, 34 three; backward 64 us two ahead, 70
+// three, 66 one.
+template <class St, int V, int PLANES> struct ConvTurn {
     static constexpr int tokens = V > 1 ? 4 : 8;
-    static constexpr int ahead = V > 1 ? 3 : 0;
+    static constexpr int ahead = V == 1 ? 0 : PLANES == 2 ? 2 : 4;
 };
 template <class St, int V, int PLANES> constexpr int conv_ring_bytes() {
-    return V > 1 ? ConvTurn<V>::ahead * ConvTurn<V>::tokens * PLANES * V * static_cast<int>(sizeof(St)) * 32 * kConvSplit : 0;
+    return V > 1 ? ConvTurn<St, V, PLANES>::ahead * ConvTurn<St, V, PLANES>::tokens * PLANES * V * static_cast<int>(sizeof(St)) * 32 * kConvSplit : 0;
 }
 template <int BYTES> __device__ __forceinline__ void conv_copy(uint32_t to, const void *from, bool in) {
     if constexpr (BYTES == 16)
@@ -43,18 +45,21 @@ __device__ __forceinline__ void conv_commit() { asm volatile("cp.async.commit_gr
 template <int N> __device__ __forceinline__ void conv_arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // The tokens t0 - (K-1) .. t0 + kConvSteps + K - 2 that start a segment, bit 0
-// the first of them; the whole warp calls it.
-template <int K> __device__ __forceinline__ uint64_t conv_starts(const int32_t *seg, long long t0, long long T) {
-    if (seg == nullptr) return 0;
-    uint64_t bits = 0;
+// the first of them.  Asked for first and put together by the whole warp once
+// the walk's own loads are on their way.
+template <int K> struct ConvStarts {
+    bool first[2];
+    __device__ __forceinline__ ConvStarts(const ConvArgs &a, long long b, long long t0) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const long long t = t0 - (K - 1) + 32 * w + (threadIdx.x & 31);
-        const bool first = t >= 0 && t < T && __ldg(seg + t) == 0;
-        bits |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, first)) << (32 * w);
+        for (int w = 0; w < 2; ++w) {
+            const long long t = t0 - (K - 1) + 32 * w + (threadIdx.x & 31);
+            first[w] = a.seg != nullptr && t >= 0 && t < a.T && __ldg(a.seg + b * a.T + t) == 0;
+        }
     }
-    return bits;
-}
+    __device__ __forceinline__ uint64_t bits() const {
+        return static_cast<uint64_t>(__ballot_sync(0xffffffffu, first[1])) << 32 | __ballot_sync(0xffffffffu, first[0]);
+    }
+};
 // Whether tap k of token i of the walk counts: no start at tokens i-k+1 .. i.
 template <int K> __device__ __forceinline__ bool conv_counts(uint64_t starts, int i, int k) {
     return ((starts >> (i + K - k)) & ((1u << k) - 1u)) == 0;
@@ -94,17 +99,18 @@ __device__ __forceinline__ void conv_token(const ConvArgs &a, long long b, long 
 // to be copied, `in` and `out` the places in the ring where the next turn is
 // copied to and read from.
 template <class St, int V, int PLANES> struct ConvFeed {
-    static constexpr int N = ConvTurn<V>::tokens, A = ConvTurn<V>::ahead, kBytes = V * static_cast<int>(sizeof(St));
+    static constexpr int N = ConvTurn<St, V, PLANES>::tokens, A = ConvTurn<St, V, PLANES>::ahead, kBytes = V * static_cast<int>(sizeof(St));
     static constexpr uint32_t kToken = PLANES * 32 * kConvSplit * kBytes;  // a token of all threads and planes
     static constexpr uint32_t kRing = A * N * kToken;
     uint32_t ring, in = 0, out = 0;
-    const St *first, *at;
+    const St *at;
     long long stride;
     int left;  // tokens that are there and not yet asked for
     __device__ ConvFeed(const char *smem, int plane, const St *from, long long st, int n)
-        : ring(smem_addr(smem) + (plane * 32 * kConvSplit + threadIdx.y * 32 + threadIdx.x) * kBytes), first(from), at(from),
+        : ring(smem_addr(smem) + (plane * 32 * kConvSplit + threadIdx.y * 32 + threadIdx.x) * kBytes), at(from),
           stride(st), left(n) {}
-    __device__ __forceinline__ void copy_turn() {
+    // `base`: any address of the plane, for tokens that are not there
+    __device__ __forceinline__ void copy_turn(const void *base) {
         const uint32_t to = ring + in;
         if (left >= N) {
 #pragma unroll
@@ -114,7 +120,7 @@ template <class St, int V, int PLANES> struct ConvFeed {
             }
         } else {
             for (int j = 0; j < N; ++j) {
-                conv_copy<kBytes>(to + j * kToken, j < left ? at : first, j < left);
+                conv_copy<kBytes>(to + j * kToken, j < left ? at : base, j < left);
                 if (j < left) at += stride;
             }
         }
@@ -173,7 +179,7 @@ __device__ __forceinline__ void conv_fwd_tokens(const typename RawOf<St, V>::T (
     }
 }
 
-template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 ? 2 : 3) conv_fwd_kernel(const ConvArgs a) {
+template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 ? 4 : 6) conv_fwd_kernel(const ConvArgs a) {
     using Feed = ConvFeed<St, V, 1>;
     constexpr int N = Feed::N, A = Feed::A;
     extern __shared__ char ring[];
@@ -182,33 +188,35 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
     const long long t0 = (static_cast<long long>(chunk) * kConvSplit + threadIdx.y) * kConvSteps;
     if (t0 >= a.T) return;
-    const uint64_t starts = conv_starts<K>(a.seg ? a.seg + b * a.T : nullptr, t0, a.T);
-    if (d >= a.D) return;
+    const ConvStarts<K> flags(a, b, t0);
+    const bool in = d < a.D;
     const int n = static_cast<int>(a.T - t0 < kConvSteps ? a.T - t0 : kConvSteps);
     Feed x(ring, 0, static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d, a.x.st, n);
     St *op = static_cast<St *>(a.o.p) + b * a.o.sb + t0 * a.o.st + d;
-    if constexpr (A > 0) {
+    if (A > 0 && in) {
 #pragma unroll
         for (int turn = 0; turn < A; ++turn) {
-            x.copy_turn();
+            x.copy_turn(a.x.p);
             conv_commit();
         }
     }
     float w[K][V], bias[V], hist[K - 1][V];  // hist[k]: x_{t-1-k}; w[k]: the tap of x_{t-k}
 #pragma unroll
-    for (int k = K - 2; k >= 0; --k) conv_token<St, V, K>(a, b, t0 - 1 - k, d, true, hist[k]);
+    for (int k = K - 2; k >= 0; --k) conv_token<St, V, K>(a, b, t0 - 1 - k, d, in, hist[k]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
-        bias[v] = a.bias ? __ldg(a.bias + d + v) : 0.0f;
+        for (int k = 0; k < K; ++k) w[k][v] = in ? __ldg(a.w + (d + v) * K + (K - 1 - k)) : 0.0f;
+        bias[v] = in && a.bias ? __ldg(a.bias + d + v) : 0.0f;
     }
+    const uint64_t starts = flags.bits();
+    if (!in) return;
     for (int turn = 0; turn * N < n; ++turn) {
         typename RawOf<St, V>::T raw[N];
         if constexpr (A > 0) {
             conv_arrived<A - 1>();
             x.read_turn(raw);
-            x.copy_turn();
+            x.copy_turn(a.x.p);
             conv_commit();
         } else {
             x.load_turn(raw);
@@ -234,14 +242,16 @@ template <int V, int K> struct ConvWalk {
 };
 
 // Tokens i .. i+N-1 of the walk add their parts to the gradients of the K tokens
-// up to each of them; the one that is complete goes out.  CLEAR: all N are the
-// walk's own, all taps count, all complete tokens are the walk's own and no
-// gradient comes in at them.
-template <class St, int V, int K, int N, bool CLEAR>
+// up to each of them; the one that is complete goes out.  kConvPlain: all taps
+// count, and no gradient comes in at the last tokens; kConvClear: all N are the
+// walk's own too, and so are all complete tokens.
+enum ConvTokens { kConvAny, kConvPlain, kConvClear };
+template <class St, int V, int K, int N, ConvTokens KIND>
 __device__ __forceinline__ void conv_bwd_tokens(const ConvArgs &a, const typename RawOf<St, V>::T (&xr)[N],
                                                 const typename RawOf<St, V>::T (&gr)[N], int i, int n, long long t0,
-                                                uint64_t starts, ConvWalk<V, K> &c, St *out, St *out0, const St *gl) {
+                                                uint64_t starts, ConvWalk<V, K> &c, St *out, long long b, long long d) {
     const long long tail = a.T - (K - 1);  // the first token of `last`
+    constexpr bool CLEAR = KIND == kConvClear, ALL = KIND != kConvAny;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         if (!CLEAR && i + j >= n + K - 1) break;
@@ -258,18 +268,18 @@ __device__ __forceinline__ void conv_bwd_tokens(const ConvArgs &a, const typenam
 #pragma unroll
             for (int k = 1; k < K; ++k) vfma<V>(c.held[k], c.w[k], g, c.held[k]);
         } else {
-            conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < a.T && t >= tail, c.held[0]);
+            conv_load<St, V>(static_cast<const St *>(a.grad_last) + (b * (K - 1) + t - tail) * a.D + d, !ALL && a.grad_last != nullptr && t < a.T && t >= tail, c.held[0]);
             if (t < a.T)
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (k == 0 || conv_counts<K>(starts, i + j, k)) vfma<V>(c.held[k], c.w[k], g, c.held[k]);
+                    if (k == 0 || ALL || conv_counts<K>(starts, i + j, k)) vfma<V>(c.held[k], c.w[k], g, c.held[k]);
         }
         if (CLEAR || i + j < n) {
             vadd<V>(c.gb, c.gb, g);
             vfma<V>(c.gw[0], g, x, c.gw[0]);
 #pragma unroll
             for (int k = 1; k < K; ++k)
-                if (CLEAR || conv_counts<K>(starts, i + j, k)) vfma<V>(c.gw[k], g, c.hist[k - 1], c.gw[k]);
+                if (ALL || conv_counts<K>(starts, i + j, k)) vfma<V>(c.gw[k], g, c.hist[k - 1], c.gw[k]);
 #pragma unroll
             for (int k = K - 2; k > 0; --k)
 #pragma unroll
@@ -281,14 +291,21 @@ __device__ __forceinline__ void conv_bwd_tokens(const ConvArgs &a, const typenam
         if (CLEAR || done >= t0)
             store_lanes<St, V>(out, c.held[K - 1]);
         else if (done < 0 && a.grad_x0 != nullptr && done >= -(K - 1))
-            store_lanes<St, V>(out0 + (done + (K - 1)) * a.D, c.held[K - 1]);
+            store_lanes<St, V>(static_cast<St *>(a.grad_x0) + (b * (K - 1) + done + (K - 1)) * a.D + d, c.held[K - 1]);
         out += a.o.st;
     }
 }
 
+// CTAs an SM.  Registers bound them: fp32 lanes spill 250 bytes a thread in the
+// 128 that four CTAs leave, and three are faster (87 us instead of 111 at
+// 8 x 2048 x 2560, K = 4); bf16 spills 70 and prefers four (64, 65 with three).
+template <class St, int V, int K> constexpr int conv_bwd_ctas() {
+    return V > 1 && K > 4 ? 2 : V > 1 && sizeof(St) == 4 ? 3 : 4;
+}
+
 // A walk reads K - 1 tokens of grad_out past its own, for the gradients of its
 // last tokens.  The walk at token 0 holds the tokens of x0 too.
-template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, K > 4 && V > 1 ? 1 : 2) conv_bwd_kernel(const ConvArgs a) {
+template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSplit, conv_bwd_ctas<St, V, K>()) conv_bwd_kernel(const ConvArgs a) {
     using Feed = ConvFeed<St, V, 2>;
     constexpr int N = Feed::N, A = Feed::A;
     extern __shared__ char ring[];  // then the sums
@@ -304,56 +321,58 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
 #pragma unroll
         for (int k = 0; k < K; ++k) c.gw[k][v] = 0.0f;
     }
-    const uint64_t starts = t0 < a.T ? conv_starts<K>(a.seg ? a.seg + b * a.T : nullptr, t0, a.T) : 0;
-    if (d < a.D && t0 < a.T) {
-        const int n = static_cast<int>(a.T - t0 < kConvSteps ? a.T - t0 : kConvSteps);
-        const long long left = a.T - t0, tail = a.T - (K - 1);
-        const int turns = (n + K - 1 + N - 1) / N;
-        Feed x(ring, 0, static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d, a.x.st, n);
-        Feed g(ring, 1, static_cast<const St *>(a.go.p) + b * a.go.sb + t0 * a.go.st + d, a.go.st,
-               n + K - 1 < left ? n + K - 1 : static_cast<int>(left));
+    const ConvStarts<K> flags(a, b, t0);
+    const bool in = d < a.D && t0 < a.T;
+    const int n = static_cast<int>(a.T - t0 < kConvSteps ? a.T - t0 : kConvSteps);
+    const long long left = a.T - t0, tail = a.T - (K - 1);
+    const int turns = in ? (n + K - 1 + N - 1) / N : 0;
+    Feed x(ring, 0, static_cast<const St *>(a.x.p) + b * a.x.sb + t0 * a.x.st + d, a.x.st, n);
+    Feed g(ring, 1, static_cast<const St *>(a.go.p) + b * a.go.sb + t0 * a.go.st + d, a.go.st,
+           n + K - 1 < left ? n + K - 1 : static_cast<int>(left));
+    if (A > 0 && in) {
+#pragma unroll
+        for (int turn = 0; turn < A; ++turn) {
+            x.copy_turn(a.x.p);
+            g.copy_turn(a.go.p);
+            conv_commit();
+        }
+    }
+    St *op = static_cast<St *>(a.o.p) + b * a.o.sb + (t0 - (K - 1)) * a.o.st + d;  // of the token that is complete
+#pragma unroll
+    for (int k = K - 2; k >= 0; --k) {
+        const long long t = t0 - 1 - k;
+        conv_token<St, V, K>(a, b, t, d, in, c.hist[k]);
+        // tokens before token 0 that are still among the last ones
+        conv_load<St, V>(static_cast<const St *>(a.grad_last) + (b * (K - 1) + t - tail) * a.D + d,
+                         in && a.grad_last != nullptr && t < 0 && t >= tail, c.held[k]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int k = 0; k < K; ++k) c.w[k][v] = in ? __ldg(a.w + (d + v) * K + (K - 1 - k)) : 0.0f;
+    const uint64_t starts = flags.bits();
+    for (int turn = 0; turn < turns; ++turn) {
+        typename RawOf<St, V>::T xr[N], gr[N];
         if constexpr (A > 0) {
-#pragma unroll
-            for (int turn = 0; turn < A; ++turn) {
-                x.copy_turn();
-                g.copy_turn();
-                conv_commit();
-            }
+            conv_arrived<A - 1>();
+            x.read_turn(xr);
+            g.read_turn(gr);
+            x.copy_turn(a.x.p);
+            g.copy_turn(a.go.p);
+            conv_commit();
+        } else {
+            x.load_turn(xr);
+            g.load_turn(gr);
         }
-        const St *gl = static_cast<const St *>(a.grad_last) + b * (K - 1) * a.D + d;
-        St *op = static_cast<St *>(a.o.p) + b * a.o.sb + (t0 - (K - 1)) * a.o.st + d;  // of the token that is complete
-        St *o0 = static_cast<St *>(a.grad_x0) + b * (K - 1) * a.D + d;
-#pragma unroll
-        for (int k = K - 2; k >= 0; --k) {
-            const long long t = t0 - 1 - k;
-            conv_token<St, V, K>(a, b, t, d, true, c.hist[k]);
-            // tokens before token 0 that are still among the last ones
-            conv_load<St, V>(gl + (t - tail) * a.D, a.grad_last != nullptr && t < 0 && t >= tail, c.held[k]);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int k = 0; k < K; ++k) c.w[k][v] = __ldg(a.w + (d + v) * K + (K - 1 - k));
-        for (int turn = 0; turn < turns; ++turn) {
-            typename RawOf<St, V>::T xr[N], gr[N];
-            if constexpr (A > 0) {
-                conv_arrived<A - 1>();
-                x.read_turn(xr);
-                g.read_turn(gr);
-                x.copy_turn();
-                g.copy_turn();
-                conv_commit();
-            } else {
-                x.load_turn(xr);
-                g.load_turn(gr);
-            }
-            const int i = turn * N;
-            if (i >= K - 1 && i + N <= n && conv_clear<K>(starts, i, N) && (a.grad_last == nullptr || t0 + i + N <= tail))
-                conv_bwd_tokens<St, V, K, N, true>(a, xr, gr, i, n, t0, starts, c, op, o0, gl);
-            else
-                conv_bwd_tokens<St, V, K, N, false>(a, xr, gr, i, n, t0, starts, c, op, o0, gl);
-            op += N * a.o.st;
-        }
+        const int i = turn * N;
+        const bool plain = conv_clear<K>(starts, i, N) && (a.grad_last == nullptr || t0 + i + N <= tail);
+        if (plain && i >= K - 1 && i + N <= n)
+            conv_bwd_tokens<St, V, K, N, kConvClear>(a, xr, gr, i, n, t0, starts, c, op, b, d);
+        else if (plain)
+            conv_bwd_tokens<St, V, K, N, kConvPlain>(a, xr, gr, i, n, t0, starts, c, op, b, d);
+        else
+            conv_bwd_tokens<St, V, K, N, kConvAny>(a, xr, gr, i, n, t0, starts, c, op, b, d);
+        op += N * a.o.st;
     }
     float(*sums)[K + 1][32 * V] = reinterpret_cast<float(*)[K + 1][32 * V]>(ring + conv_ring_bytes<St, V, 2>());
 #pragma unroll
