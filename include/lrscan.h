@@ -449,7 +449,8 @@ size_t lrscan_gates_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype, 
  * state [S, D], updated in place (slots NULL: row b).  A negative slot is a
  * request that is not there: its output row is zeros.  A slot of S or more
  * does the same and is reported as LRSCAN_EINVAL by lrscan_sync_check.  Two
- * requests must not share a slot.
+ * requests must not share a slot.  A step does not restart: the first token of
+ * a document goes in by lrscan_fwd_gates, its segment_pos 0.
  */
 int lrscan_step_gates(const lrscan_rows *r, const lrscan_rows *i, const lrscan_rows *x,
                       const float *lam, float c, float *state, const int32_t *slots, const lrscan_rows *out,

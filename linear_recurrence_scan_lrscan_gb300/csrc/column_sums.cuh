@@ -2,7 +2,9 @@
 // kernels that leave one row of partial sums a tile: a CTA takes 32 columns,
 // its 32 warps every 32nd row of the CTA's slice of rows, and their sums are
 // added in warp order.  Many rows are cut in slices, whose sums take the rows
-// after the matrix and are then summed alike.
+// after the matrix and are then summed alike.  Eight loads in flight a thread, and a
+// slice for every 256 rows; latency bounds it, and each of its one or two launches
+// begins while the kernel before ends.
 #pragma once
 
 #include <cuda_runtime.h>

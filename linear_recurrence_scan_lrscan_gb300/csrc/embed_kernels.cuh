@@ -13,6 +13,13 @@
 // rows, the zeros keep the memory busy.  A run of one id is summed by the CTA it
 // starts in, up to 32 tokens past its stretch; a longer run takes every CTA it
 // touches, which leave fp32 sums, and the third kernel adds those up.
+//
+// Measured backward (of the measured copy bandwidth; the bytes are grad_out and
+// the whole table): 16384 tokens into 32768 x 2560 fp32 95 us, 65 %, bf16 68 us,
+// 54 %; 2048 tokens 40 us, 65 %; 3001 tokens into 5003 x 777 bf16 25 us.  At the first
+// of these the sort takes 19 us and the sums 34 alone, mostly waiting for rows in
+// runs of ids; zeros with one CTA an SM 103 us, half a CTA 118.  Small
+// cases are three launches and the sort's barriers between CTAs (10 us for 32 tokens).
 #pragma once
 
 #include "embed_args.h"
@@ -42,6 +49,10 @@ template <class St, int V> __device__ __forceinline__ void row_load(const St *p,
     }
 }
 
+// A thread moves V lanes of up to four rows, all loaded before the first is
+// stored.  Bound by bytes, and by the rows' order in the table: 16384 rows of
+// 2560 from fp32 to bf16 30 us, 70 % of the measured copy bandwidth (25 us on the
+// device alone); 32 rows 4.1 us a call, which is the launch.
 constexpr int kRowsPerThread = 4;
 
 template <class W, class O, int V, int R> __global__ void __launch_bounds__(256) embed_fwd_kernel(const EmbedArgs a) {

@@ -20,6 +20,21 @@
 // tiles in ahead (bulk tensor copies into S stages) and three fold entering
 // states ahead, from the moment a tile is named.  What a token's second walk
 // needs stays in registers, so that HBM carries each element once.
+//
+// What it measured (forward / backward, of the measured copy bandwidth; forward
+// moves 4 elements a token and lane, backward 7):
+//
+//   8 x 2048 x 2560 fp32          107 / 182 us   92 / 95 %   bytes
+//   8 x 2048 x 2560 bf16           72 / 123 us   68 / 70 %   instructions: 16 warps an SM
+//   1 x 65536 x 2560 fp32, packed 492 / 898 us   80 / 77 %   the chain of entering states
+//   1 x 2^18 x 256 fp32           213 / 338 us   74 / 82 %   that chain, four lane tiles
+//   1 x 2^20 x 64 bf16            208 / 264 us   38 / 52 %   that chain, one lane tile
+//
+// Measured against other splits at 8 x 2048 x 2560 bf16: 32-token tiles make the
+// fold warps the bound (84 / 348); two teams of eight warps 100 / 214; group maps
+// made by the teams spill (85 forward).  Radix 16 of the tree beats 8 for one lane
+// tile (208 / 264 us against 365 / 377) and loses 3 to 5 % at 65536 x 2560; a
+// fourth level changes neither by more than 4 %.
 #pragma once
 
 #include "gates_args.h"
@@ -103,7 +118,8 @@ __device__ __forceinline__ void decay2(const float (&k)[2], const float (&rg)[2]
 }
 
 // Before a launch whose tiles follow one another: nothing is published (all-ones
-// words), and every lane's rate is computed once.
+// words), and every lane's rate is computed once.  Bound by its launch,
+// which that of the main kernel overlaps.
 __global__ void __launch_bounds__(256) gates_begin_kernel(uint4 *words, long long n, const float *lam, float c, long long D,
                                                           float *rate) {
     const long long first = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, step = 256LL * gridDim.x;
@@ -517,7 +533,8 @@ __device__ __forceinline__ float load_one(const St *p, bool in) {
     load_lanes_global<St, 1>(p, x);
     return x[0];
 }
-// SLOW: lanes past the last are left out.
+// SLOW: lanes past the last are left out.  Outputs go from registers: two lanes a
+// thread fill whole 128-byte lines a warp in bf16, 256 bytes in fp32.
 template <class St, bool BULK, bool SLOW>
 __device__ __forceinline__ void store_pair(St *row, int lane, const bool (&in)[2], float y0, float y1) {
     if constexpr (BULK) {

@@ -76,8 +76,8 @@ def lrscan_fwd_gates(r, i, x, lam, *, c: float = 8.0, h0=None, segment_pos=None,
                      want_saved: bool = False, workspace=None, stream=None):
     """Gated recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t with
     a_t = exp(-c softplus(lam) sigmoid(r_t)), from the fp32 [B, D] state h0,
-    restarting (a_t = 0) where the int32 [B, T] segment_pos is 0; r, i, x
-    [B, T, D], lam fp32 [D].  Returns (out, last, saved): the states in the
+    restarting (a_t = 0, so the token's input enters whole) where the int32 [B, T]
+    segment_pos is 0; r, i, x [B, T, D], lam fp32 [D].  Returns (out, last, saved): the states in the
     storage dtype, the fp32 [B, D] final state, and (want_saved) the fp32 states
     before tokens 0, 16, 32, ... that the backward needs, else None."""
     return (_binding or _native()).fwd_gates(r, i, x, lam, c, h0, segment_pos, out, last, saved, want_saved, workspace, stream)
@@ -96,7 +96,8 @@ def lrscan_bwd_gates(r, i, x, lam, saved, grad_out, *, c: float = 8.0, segment_p
 def lrscan_step_gates(r, i, x, lam, state, *, slots=None, c: float = 8.0, out=None, stream=None):
     """One token of each of B requests: r, i, x [B, D]; request b's state is row
     slots[b] (int32 [B]; row b without slots) of the fp32 pool state [S, D],
-    updated in place.  Returns out [B, D]; a negative slot gives zeros."""
+    updated in place.  Returns out [B, D]; a negative slot gives zeros.  A step
+    does not restart: a document's first token is :func:`lrscan_fwd_gates`'s."""
     return (_binding or _native()).step_gates(r, i, x, lam, state, slots, c, out, stream)
 
 

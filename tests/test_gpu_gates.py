@@ -315,3 +315,29 @@ def test_gates_refusals():
         with pytest.raises(what):
             call()
     assert L.lrscan_sync_check() == 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gates_rows_that_share_memory(dt):
+    # one row for all batch rows, one token for all tokens: strides of zero
+    s = draw(3, 150, 64, dt, 21, carry=True)
+    s["r"] = s["r"][:1].expand(3, -1, -1)
+    s["x"] = s["x"][:, :1].expand(-1, 150, -1)
+    s["go"] = s["go"][:1, :1].expand(3, 150, -1)
+    check(s)
+
+
+def test_gates_gradient_of_broadcast_inputs():
+    # the gradient of what was broadcast is the sum over where it went
+    s = draw(3, 90, 64, "f32", 22)
+    r, x, i = (s[k].clone().requires_grad_() for k in ("r", "x", "i"))
+    one_r, one_x = s["r"][:1].clone().requires_grad_(), s["x"][:, :1].clone().requires_grad_()
+    L.gate_scan(one_r.expand(3, -1, -1), i, one_x.expand(-1, 90, -1), s["lam"])[0].sum().backward()
+    with torch.no_grad():
+        r.copy_(s["r"][:1].expand(3, -1, -1))
+        x.copy_(s["x"][:, :1].expand(-1, 90, -1))
+    L.gate_scan(r, s["i"], x, s["lam"])[0].sum().backward()
+    # the same gradients, summed over 3 rows or 90 tokens in fp32 either way
+    for got, parts, dim, n in ((one_r.grad, r.grad, 0, 3), (one_x.grad, x.grad, 1, 90)):
+        bound = n * 2.0 ** -23 * parts.abs().sum(dim, keepdim=True)
+        assert ((got - parts.sum(dim, keepdim=True)).abs() <= bound + 1e-30).all()
