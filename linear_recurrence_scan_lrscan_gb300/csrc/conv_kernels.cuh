@@ -17,10 +17,10 @@
 // Forward moves 2 elements a token and channel, backward 3 and K + 1 fp32 partial
 // sums a CTA and channel.  Measured (of the measured copy bandwidth), K = 4:
 //
-//   8 x 2048 x 2560 fp32           55 /  87 us   89 / 85 %   bytes
-//   8 x 2048 x 2560 bf16, packed   33 /  64 us   74 / 58 %   latency: 128 registers a
+//   8 x 2048 x 2560 fp32           53 /  85 us   93 / 87 %   bytes
+//   8 x 2048 x 2560 bf16, packed   31 /  62 us   79 / 60 %   latency: 128 registers a
 //                                                 thread leave the backward 16 warps an SM
-//   3 x 777 x 1001 bf16, packed   8.4 /  15 us               two launches, 2-byte accesses
+//   3 x 777 x 1001 bf16, packed   6.3 /  14 us               two launches, 2-byte accesses
 //
 // Conditions on every tap cost 135 us in the bf16 backward, loads straight to
 // registers 83; eight walks a CTA 70, two 66.
@@ -36,7 +36,7 @@ namespace lrscan {
 // (V > 1) come in through shared memory: each thread copies the lanes it will
 // read itself, so that nothing waits but its own copies, and what is on its way
 // takes no registers.  Others are loaded a turn at a time.  Forward 8 x 2048 x
-// 2560 bf16: 33 us four turns ahead, 34 three; backward 64 us two ahead, 70
+// 2560 bf16, launches apart: 33 us four turns ahead, 34 three; backward 64 us two ahead, 70
 // three, 66 one.
 template <class St, int V, int PLANES> struct ConvTurn {
     static constexpr int tokens = V > 1 ? 4 : 8;
@@ -198,6 +198,8 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
     const long long b = blockIdx.y;
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
     const long long t0 = (static_cast<long long>(chunk) * kConvSplit + threadIdx.y) * kConvSteps;
+    pdl_wait();
+    pdl_trigger();
     if (t0 >= a.T) return;
     const ConvStarts<K> flags(a, b, t0);
     const bool in = d < a.D;
@@ -324,6 +326,7 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
     const long long b = blockIdx.y;
     const long long d = (static_cast<long long>(lanes) * 32 + threadIdx.x) * V;
     const long long t0 = (static_cast<long long>(chunk) * kConvSplit + threadIdx.y) * kConvSteps;
+    pdl_wait();
     pdl_trigger();  // the reduction waits for this grid's end all the same
     ConvWalk<V, K> c;
 #pragma unroll
@@ -407,9 +410,11 @@ template <class St, int V, int K> __global__ void __launch_bounds__(32 * kConvSp
 
 // One token of each of B requests: a thread a channel, its window's tokens loaded
 // together.  Bound by the launch and one round trip to memory (32 x 2560 bf16, K =
-// 4: 3.8 us a call; its 1.2 MB take 0.2 us).
+// 4: 1.6 us in a captured graph, 4.4 a call; its 1.4 MB take 0.2 us).
 template <class St, int K> __global__ void __launch_bounds__(256) conv_step_kernel(const ConvStep g) {
     const long long d = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
     if (d >= g.D) return;
     float w[K];
 #pragma unroll

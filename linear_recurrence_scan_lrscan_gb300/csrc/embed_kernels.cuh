@@ -6,19 +6,20 @@
 // Backward in three kernels.  The first sorts the tokens by id, stably, by digits
 // of up to 9 bits, on one cluster: each warp counts the digits of its own stretch
 // of tokens, the counts become every warp's first places, and the warp moves its
-// tokens there.  The second begins beside it: one CTA an SM writes the zeros of
+// tokens there.  The second begins beside it: two CTAs an SM write the zeros of
 // the rows that have no token, most of what is written for a large table, and
-// finds its rows' tokens by reading all ids once.  The others wait for the sort
+// find their rows' tokens by reading all ids once.  The others wait for the sort
 // and sum the rows of equal stretches of the sorted tokens; while they wait for
 // rows, the zeros keep the memory busy.  A run of one id is summed by the CTA it
 // starts in, up to 32 tokens past its stretch; a longer run takes every CTA it
 // touches, which leave fp32 sums, and the third kernel adds those up.
 //
 // Measured backward (of the measured copy bandwidth; the bytes are grad_out and
-// the whole table): 16384 tokens into 32768 x 2560 fp32 95 us, 65 %, bf16 68 us,
-// 54 %; 2048 tokens 40 us, 65 %; 3001 tokens into 5003 x 777 bf16 25 us.  At the first
+// the whole table): 16384 tokens into 32768 x 2560 fp32 93 us, 67 %, bf16 66 us,
+// 56 %; 2048 tokens 38 us, 69 %; 3001 tokens into 5003 x 777 bf16 23 us.  At the first
 // of these the sort takes 19 us and the sums 34 alone, mostly waiting for rows in
-// runs of ids; zeros with one CTA an SM 103 us, half a CTA 118.  Small
+// runs of ids; zeros with one CTA an SM instead
+// of two 4 us more, with half a CTA 19.  Small
 // cases are three launches and the sort's barriers between CTAs (10 us for 32 tokens).
 #pragma once
 
@@ -51,14 +52,16 @@ template <class St, int V> __device__ __forceinline__ void row_load(const St *p,
 
 // A thread moves V lanes of up to four rows, all loaded before the first is
 // stored.  Bound by bytes, and by the rows' order in the table: 16384 rows of
-// 2560 from fp32 to bf16 30 us, 70 % of the measured copy bandwidth (25 us on the
-// device alone); 32 rows 4.1 us a call, which is the launch.
+// 2560 from fp32 to bf16 28 us, 76 % of the measured copy bandwidth (30 without
+// programmatic launches); 32 rows 2.8 us a call, which is the launch.
 constexpr int kRowsPerThread = 4;
 
 template <class W, class O, int V, int R> __global__ void __launch_bounds__(256) embed_fwd_kernel(const EmbedArgs a) {
     const unsigned nd = static_cast<unsigned>((a.D + 32 * V - 1) / (32 * V));
     const long long d = (static_cast<long long>(blockIdx.x % nd) * 32 + threadIdx.x) * V;
     const long long n0 = static_cast<long long>(blockIdx.x / nd) * (8 * R) + threadIdx.y;
+    pdl_wait();
+    pdl_trigger();
     if (d >= a.D) return;
     float x[R][V];
 #pragma unroll
@@ -132,6 +135,7 @@ embed_sort_kernel(const EmbedArgs a) {
                                          // then the tokens held: [2] x [key, val] x [a.held]
     __shared__ uint32_t base[kSortBins], totals[kSortBins];
     __shared__ uint32_t sums[kSortBins / 32];
+    pdl_wait();  // before the trigger: the second kernel's zeros wait for nothing else
     pdl_trigger();
     const int bins = 1 << a.bits, row = bins + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -46,11 +46,9 @@ template <class St, int V, int K> int run(const ConvArgs &a, int dir) {
         if (a.grad_x0) s.grad_x0 = static_cast<char *>(a.grad_x0) + off;
         if (a.part) s.part = a.part + b0 * a.chunks * (K + 1) * a.D;
         const dim3 grid(s.ndt * a.chunks, static_cast<unsigned>(s.B));
-        if (dir == 0)
-            conv_fwd_kernel<St, V, K><<<grid, block, smem_f, a.stream>>>(s);
-        else
-            conv_bwd_kernel<St, V, K><<<grid, block, smem_b, a.stream>>>(s);
-        if (cudaGetLastError() != cudaSuccess) return 1;
+        const cudaError_t e = dir == 0 ? launch_pdl(conv_fwd_kernel<St, V, K>, grid, block, smem_f, a.stream, s)
+                                       : launch_pdl(conv_bwd_kernel<St, V, K>, grid, block, smem_b, a.stream, s);
+        if (e != cudaSuccess) return 1;
     }
     return 0;
 }
@@ -73,20 +71,21 @@ int pick(const ConvArgs &a, int K, int dtype, int dir) {
     return a.vec ? taps<bf16_t, 4>(a, K, dir) : taps<bf16_t, 1>(a, K, dir);
 }
 
-template <class St, int K> void step(const ConvStep &a, dim3 grid) { conv_step_kernel<St, K><<<grid, 256, 0, a.stream>>>(a); }
+template <class St, int K> int step(const ConvStep &a, dim3 grid) {
+    return launch_pdl(conv_step_kernel<St, K>, grid, dim3(256), 0, a.stream, a) != cudaSuccess;
+}
 
 template <class St> int step_taps(const ConvStep &a, int K, dim3 grid) {
     switch (K) {
-        case 2: step<St, 2>(a, grid); break;
-        case 3: step<St, 3>(a, grid); break;
-        case 4: step<St, 4>(a, grid); break;
-        case 5: step<St, 5>(a, grid); break;
-        case 6: step<St, 6>(a, grid); break;
-        case 7: step<St, 7>(a, grid); break;
-        case 8: step<St, 8>(a, grid); break;
+        case 2: return step<St, 2>(a, grid);
+        case 3: return step<St, 3>(a, grid);
+        case 4: return step<St, 4>(a, grid);
+        case 5: return step<St, 5>(a, grid);
+        case 6: return step<St, 6>(a, grid);
+        case 7: return step<St, 7>(a, grid);
+        case 8: return step<St, 8>(a, grid);
         default: return 1;
     }
-    return cudaGetLastError() != cudaSuccess;
 }
 
 }  // namespace

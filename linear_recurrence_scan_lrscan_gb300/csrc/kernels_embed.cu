@@ -15,13 +15,12 @@ template <class W, class O, int V> int fwd(const EmbedArgs &a) {
     const dim3 block(32, 8);
     // several rows a thread once the rows alone keep the SMs busy
     const long long few = (a.N + 7) / 8 * nd, many = (a.N + 8 * kRowsPerThread - 1) / (8 * kRowsPerThread) * nd;
-    if (many >= 4LL * a.sm_count) {
-        if (many > 0x7fffffffLL) return 1;
-        embed_fwd_kernel<W, O, V, kRowsPerThread><<<static_cast<unsigned>(many), block, 0, a.stream>>>(a);
-    } else {
-        embed_fwd_kernel<W, O, V, 1><<<static_cast<unsigned>(few), block, 0, a.stream>>>(a);
-    }
-    return cudaGetLastError() != cudaSuccess;
+    if (many > 0x7fffffffLL) return 1;
+    const cudaError_t e =
+        many >= 4LL * a.sm_count
+            ? launch_pdl(embed_fwd_kernel<W, O, V, kRowsPerThread>, dim3(static_cast<unsigned>(many)), block, 0, a.stream, a)
+            : launch_pdl(embed_fwd_kernel<W, O, V, 1>, dim3(static_cast<unsigned>(few)), block, 0, a.stream, a);
+    return e != cudaSuccess;
 }
 
 template <class G, class O, int V> int bwd_vec(EmbedArgs a) {
@@ -35,8 +34,7 @@ template <class G, class O, int V> int bwd_vec(EmbedArgs a) {
         smem += static_cast<int>(held * 16);
     }
     if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) return 1;
-    embed_sort_kernel<<<kSortCtas, kSortWarps * 32, smem, a.stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return 1;
+    if (launch_pdl(embed_sort_kernel, dim3(kSortCtas), dim3(kSortWarps * 32), smem, a.stream, a) != cudaSuccess) return 1;
     const long long lanes = (a.D + V - 1) / V;
     constexpr int U = V == 1 ? 4 : 1;
     const long long ny = (lanes + 512 * U - 1) / (512 * U);  // a row's lanes in equal parts
