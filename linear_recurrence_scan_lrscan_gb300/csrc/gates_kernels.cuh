@@ -16,7 +16,8 @@
 // agree bit for bit: maps of tiles and of groups of 16 tiles, and the state
 // after every 256 tiles.  One CTA an SM takes tiles by ticket, all lanes'
 // earliest tiles first, so a tile waits for running CTAs alone.  Four teams
-// work on four tiles, so that one computes while another waits; one warp copies
+// work on four tiles (three where registers are worth more), so that one computes
+// while another waits; one warp copies
 // tiles in ahead (bulk tensor copies into S stages) and three fold entering
 // states ahead, from the moment a tile is named.  What a token's second walk
 // needs stays in registers, so that HBM carries each element once.
@@ -25,10 +26,12 @@
 // moves 4 elements a token and lane, backward 7):
 //
 //   8 x 2048 x 2560 fp32          107 / 182 us   92 / 95 %   bytes
-//   8 x 2048 x 2560 bf16           72 / 123 us   68 / 70 %   instructions: 16 warps an SM
-//   1 x 65536 x 2560 fp32, packed 492 / 898 us   80 / 77 %   the chain of entering states
-//   1 x 2^18 x 256 fp32           213 / 338 us   74 / 82 %   that chain, four lane tiles
+//   8 x 2048 x 2560 bf16           71 / 123 us   70 / 70 %   instructions, and chains of
+//     the same, in segments        80 / 163 us   62 / 53 %   them: 12 to 16 warps an SM
+//   1 x 65536 x 2560 fp32, packed 492 / 853 us   80 / 81 %   the chain of entering states
+//   1 x 2^18 x 256 fp32           213 / 339 us   74 / 82 %   that chain, four lane tiles
 //   1 x 2^20 x 64 bf16            208 / 264 us   38 / 52 %   that chain, one lane tile
+//   3 x 777 x 1001 bf16, packed    16 /  26 us               dependent launches, latency
 //
 // Measured against other splits at 8 x 2048 x 2560 bf16: 32-token tiles make the
 // fold warps the bound (84 / 348); two teams of eight warps 100 / 214; group maps
@@ -773,6 +776,18 @@ gates_fwd_kernel(const GatesArgs g, const __grid_constant__ CUtensorMap mr, cons
 //   grad_lam = sigmoid(lam) / softplus(lam) sum q
 // (first token of a segment: a = 0 and s = 1 are constants, so q = 0).
 // ----------------------------------------------------------------------------
+// A segment's start is taken by selects, not branches, so that the sixteen tokens
+// of a walk stay one block that the compiler can interleave (1 x 65536 x 2560 fp32
+// in segments of 1500 tokens: 855 us, 898 with branches; 3 x 777 x 1001 bf16 26 and
+// 29; 8 x 2048 x 2560 bf16 163 and 161, where the selects lengthen the chains: 150
+// without them.  The forward, with one chain a walk, is 2 % faster with branches.
+// A path of its own for warps without a start: 214, as warps on different paths
+// miss the instruction cache).
+__device__ __forceinline__ void select2(float (&x)[2], bool yes, float y) {
+    x[0] = yes ? y : x[0];
+    x[1] = yes ? y : x[1];
+}
+
 // First walk, last token to first: the decays, and the adjoint's map over the
 // tokens.
 template <class St, class Geo, bool BULK, bool SEG, bool SLOW>
@@ -790,15 +805,13 @@ __device__ __forceinline__ void gates_bwd_decays(const GatesArgs &g, const char 
         sigmoid2(rg, r);
         decay_only2<SLOW>(k, rg, G, a[l], m);
         if (SLOW && l >= left) a[l][0] = a[l][1] = 1.0f;
-        if (SEG && ((first >> l) & 1u)) {
-            a[l][0] = a[l][1] = 0.0f;
-            P[0] = P[1] = 0.0f;
-            Q[0] = Q[1] = 0.0f;
-        } else {
-            add_x2(Q[0], Q[1], Q[0], Q[1], go[0], go[1]);
-            mul_x2(Q[0], Q[1], Q[0], Q[1], a[l][0], a[l][1]);
-            mul_x2(P[0], P[1], P[0], P[1], a[l][0], a[l][1]);
-        }
+        const bool start = SEG && ((first >> l) & 1u);
+        if (SEG) select2(a[l], start, 0.0f);
+        add_x2(Q[0], Q[1], Q[0], Q[1], go[0], go[1]);
+        mul_x2(Q[0], Q[1], Q[0], Q[1], a[l][0], a[l][1]);
+        mul_x2(P[0], P[1], P[0], P[1], a[l][0], a[l][1]);
+        if (SEG) select2(P, start, 0.0f);  // an infinity times 0 would pass
+        if (SEG) select2(Q, start, 0.0f);
     }
 }
 
@@ -813,10 +826,8 @@ __device__ __forceinline__ void gates_bwd_adjoints(const GatesArgs &g, const cha
         float go[2];
         plane_pair<St, Geo, BULK>(stage, 3, row0 + l, g.go, ag, l, lane, go);
         add_x2(go[0], go[1], go[0], go[1], cc[0], cc[1]);
-        if (SEG && ((first >> l) & 1u))
-            cc[0] = cc[1] = 0.0f;
-        else
-            mul_x2(cc[0], cc[1], go[0], go[1], a[l][0], a[l][1]);
+        mul_x2(cc[0], cc[1], go[0], go[1], a[l][0], a[l][1]);
+        if (SEG) select2(cc, (first >> l) & 1u, 0.0f);
         a[l][0] = go[0];
         a[l][1] = go[1];
     }
@@ -841,11 +852,13 @@ __device__ __forceinline__ void gates_bwd_grads(const GatesArgs &g, const char *
         plane_pair<St, Geo, BULK>(stage, 0, row0 + l, g.r, ar, l, lane, r);
         plane_pair<St, Geo, BULK>(stage, 1, row0 + l, g.i, ai, l, lane, i);
         plane_pair<St, Geo, BULK>(stage, 2, row0 + l, g.x, ax, l, lane, x);
+        const bool start = SEG && ((first >> l) & 1u);
+        if (SEG) select2(r, start, 0.0f);  // whatever the gate holds, q and grad_r are 0 there
         sigmoid2(rg, r);
         sigmoid2(ig, i);
         decay2<SLOW>(k, rg, G, a, sq, rs);
-        const bool start = SEG && ((first >> l) & 1u);
-        if (start) sq[0] = sq[1] = 1.0f;
+        if (SEG) select2(sq, start, 1.0f);
+        if (SEG) select2(h, start, 0.0f);
         mul_x2(ix[0], ix[1], ig[0], ig[1], x[0], x[1]);
         // grad_x = g s ig, grad_i = g s ig x (1 - ig)
         mul_x2(yx[0], yx[1], gt[l][0], gt[l][1], sq[0], sq[1]);
@@ -853,23 +866,19 @@ __device__ __forceinline__ void gates_bwd_grads(const GatesArgs &g, const char *
         mul_x2(yi[0], yi[1], yx[0], yx[1], ix[0], ix[1]);
         mul_x2(yi[0], yi[1], yi[0], yi[1], z[0], z[1]);
         mul_x2(yx[0], yx[1], yx[0], yx[1], ig[0], ig[1]);
-        if (start) {
-            yr[0] = yr[1] = 0.0f;
-            mul_x2(h[0], h[1], ix[0], ix[1], sq[0], sq[1]);
-        } else {
-            // q = G a g (ig x a / s - h)
-            mul_x2(w[0], w[1], ix[0], ix[1], a[0], a[1]);
-            mul_x2(w[0], w[1], w[0], w[1], rs[0], rs[1]);
-            fma_x2(w[0], w[1], h[0], h[1], -1.0f, -1.0f, w[0], w[1]);
-            mul_x2(q[0], q[1], G[0], G[1], a[0], a[1]);
-            mul_x2(q[0], q[1], q[0], q[1], gt[l][0], gt[l][1]);
-            mul_x2(q[0], q[1], q[0], q[1], w[0], w[1]);
-            add_x2(ql[0], ql[1], ql[0], ql[1], q[0], q[1]);
-            fma_x2(z[0], z[1], rg[0], rg[1], -1.0f, -1.0f, 1.0f, 1.0f);
-            mul_x2(yr[0], yr[1], q[0], q[1], z[0], z[1]);
-            mul_x2(ix[0], ix[1], ix[0], ix[1], sq[0], sq[1]);
-            fma_x2(h[0], h[1], a[0], a[1], h[0], h[1], ix[0], ix[1]);
-        }
+        // q = G a g (ig x a / s - h)
+        mul_x2(w[0], w[1], ix[0], ix[1], a[0], a[1]);
+        mul_x2(w[0], w[1], w[0], w[1], rs[0], rs[1]);
+        fma_x2(w[0], w[1], h[0], h[1], -1.0f, -1.0f, w[0], w[1]);
+        mul_x2(q[0], q[1], G[0], G[1], a[0], a[1]);
+        mul_x2(q[0], q[1], q[0], q[1], gt[l][0], gt[l][1]);
+        mul_x2(q[0], q[1], q[0], q[1], w[0], w[1]);
+        if (SEG) select2(q, start, 0.0f);
+        add_x2(ql[0], ql[1], ql[0], ql[1], q[0], q[1]);
+        fma_x2(z[0], z[1], rg[0], rg[1], -1.0f, -1.0f, 1.0f, 1.0f);
+        mul_x2(yr[0], yr[1], q[0], q[1], z[0], z[1]);
+        mul_x2(ix[0], ix[1], ix[0], ix[1], sq[0], sq[1]);
+        fma_x2(h[0], h[1], a[0], a[1], h[0], h[1], ix[0], ix[1]);
         store_pair<St, BULK, SLOW>(gr, lane, in, yr[0], yr[1]);
         store_pair<St, BULK, SLOW>(gi, lane, in, yi[0], yi[1]);
         store_pair<St, BULK, SLOW>(gx, lane, in, yx[0], yx[1]);

@@ -1,5 +1,7 @@
 // Launchers of the gated-recurrence kernels, the single-token kernel and the
 // reduction of the lam gradient.
+#include <type_traits>
+
 #include "column_sums.cuh"
 #include "gates_args.h"
 #include "gates_kernels.cuh"
@@ -33,11 +35,11 @@ template <class Kern> int resident(Kern kern, int threads, int smem, int (&cache
     return cache[dev];
 }
 
-template <class St, bool BULK, bool SEG> int fwd(const GatesLaunch &L, int sm_count) {
-    using Sh = Shape<St, 0>;
-    using Geo = GatesGeo<St, Sh::teams, Sh::stages, 3, BULK>;
+template <class St, int TEAMS, bool BULK, bool SEG> int fwd(const GatesLaunch &L, int sm_count) {
+    constexpr int S = Shape<St, 0>::stages;
+    using Geo = GatesGeo<St, TEAMS, S, 3, BULK>;
     static int cache[kMaxDev] = {};
-    auto kern = gates_fwd_kernel<St, Sh::teams, Sh::stages, BULK, SEG>;
+    auto kern = gates_fwd_kernel<St, TEAMS, S, BULK, SEG>;
     int dev = 0;
     const int fit = resident(kern, Geo::kThreads, Geo::kBytes, cache, &dev);
     if (fit == 0) return 1;
@@ -59,11 +61,23 @@ template <class St, bool BULK, bool SEG> int bwd(const GatesLaunch &L, int sm_co
                       L.stream, L.a, L.maps[0], L.maps[1], L.maps[2], L.maps[3]) != cudaSuccess;
 }
 
+template <class St, int TEAMS> int pick_fwd(const GatesLaunch &L, int sm_count) {
+    const bool seg = L.a.seg != nullptr;
+    if (L.bulk) return seg ? fwd<St, TEAMS, true, true>(L, sm_count) : fwd<St, TEAMS, true, false>(L, sm_count);
+    return seg ? fwd<St, TEAMS, false, true>(L, sm_count) : fwd<St, TEAMS, false, false>(L, sm_count);
+}
+
 template <class St> int pick(const GatesLaunch &L, int dir, int sm_count) {
     const bool seg = L.a.seg != nullptr;
     if (dir == 0) {
-        if (L.bulk) return seg ? fwd<St, true, true>(L, sm_count) : fwd<St, true, false>(L, sm_count);
-        return seg ? fwd<St, false, true>(L, sm_count) : fwd<St, false, false>(L, sm_count);
+        // Three teams of bf16 lanes have 128 registers a thread and spill nothing (8 x
+        // 2048 x 2560: 71 us, 72 with four; in segments 80 and 86; 3 x 777 x 1001 16.5
+        // and 18.4).  With few lane tiles for the CTAs a tile mostly waits for those
+        // before it, and a fourth team hides more of that (1 x 2^20 x 64: 208, 243 with
+        // three).  fp32 moves too many bytes for it to matter.
+        if constexpr (std::is_same<St, bf16_t>::value)
+            if (4LL * L.a.nl >= sm_count) return pick_fwd<St, 3>(L, sm_count);
+        return pick_fwd<St, Shape<St, 0>::teams>(L, sm_count);
     }
     if (L.bulk) return seg ? bwd<St, true, true>(L, sm_count) : bwd<St, true, false>(L, sm_count);
     return seg ? bwd<St, false, true>(L, sm_count) : bwd<St, false, false>(L, sm_count);

@@ -341,3 +341,26 @@ def test_gates_gradient_of_broadcast_inputs():
     for got, parts, dim, n in ((one_r.grad, r.grad, 0, 3), (one_x.grad, x.grad, 1, 90)):
         bound = n * 2.0 ** -23 * parts.abs().sum(dim, keepdim=True)
         assert ((got - parts.sum(dim, keepdim=True)).abs() <= bound + 1e-30).all()
+
+
+@pytest.mark.parametrize("packed", [0, 20])
+@pytest.mark.parametrize("D", [64, 33])
+def test_gates_many_lane_tiles(D, packed):
+    # a lane tile for every fourth SM and more: bf16 forward takes fewer, wider teams
+    check(draw(40, 150, D, "bf16", 23, carry=True, packed=packed))
+
+
+@pytest.mark.parametrize("D", [64, 65])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gates_restart_stops_a_nan_gate(dt, D):
+    s = draw(1, 200, D, dt, 24)
+    s["seg"] = torch.ones((1, 200), dtype=torch.int32, device="cuda")
+    s["seg"][:, [0, 50, 130]] = 0
+    s["r"][:, 100] = float("nan")
+    s["r"][:, 130] = float("nan")      # a segment's first token: its decay is not used
+    out, last, saved = run_fwd(s)
+    assert torch.isfinite(out[:, :100]).all() and torch.isnan(out[:, 100:130]).all()
+    assert torch.isfinite(out[:, 130:]).all() and torch.isfinite(last).all()
+    for grad in run_bwd(s, saved)[:3]:
+        # back from token 100 to its segment's start, and in grad_r on to its end
+        assert torch.isfinite(grad[:, :50]).all() and torch.isfinite(grad[:, 130:]).all()
