@@ -16,11 +16,11 @@
 // agree bit for bit: maps of tiles and of groups of 16 tiles, and the state
 // after every 256 tiles.  One CTA an SM takes tiles by ticket, all lanes'
 // earliest tiles first, so a tile waits for running CTAs alone.  Four teams
-// work on four tiles (three where registers are worth more), so that one computes
-// while another waits; one warp copies
-// tiles in ahead (bulk tensor copies into S stages) and three fold entering
-// states ahead, from the moment a tile is named.  What a token's second walk
-// needs stays in registers, so that HBM carries each element once.
+// work on four tiles (three where registers are worth more), so that one
+// computes while another waits; one warp copies tiles in ahead (bulk tensor
+// copies into S stages) and three fold entering states ahead, from the moment a
+// tile is named.  What a token's second walk needs stays in registers, so that
+// HBM carries each element once.
 //
 // What it measured (forward / backward, of the measured copy bandwidth; forward
 // moves 4 elements a token and lane, backward 7):
